@@ -317,6 +317,130 @@ mla_status mla_run_noalloc(const mla_dims* dims, int32_t batch, const int32_t* q
                            const void* q_pe, const void* cache, void* out, float* lse, void* stream,
                            int32_t* status_out);
 
+/* ------------------------------------------------------------------ speculative trees
+ * A speculative step may draft a TREE of continuations per row instead of one chain.  Row
+ * b's q_b step tokens are then the nodes of its tree(s): node i is token t = qo_indptr[b]
+ * + i, its latent row is key c_b + i of the row (c_b = k_b - q_b context keys), and
+ * parents[t] is the index within the row of the node it continues, smaller than i, or -1
+ * for a root.  Node i sees the row's context, its ancestors and itself:
+ *     j < c_b,  or  j = c_b + a  with a in {i, parent(i), parent(parent(i)), ...}
+ * so a chain (parents[t] = i - 1) is the causal step of mla_plan.
+ * The step of a serving loop: mla_plan_tree_update, then per layer mla_run_append, then
+ * mla_verify_tree on the target's probabilities and mla_compact_kv on all layers' caches. */
+
+/* Most nodes of a row that is not a chain (a chain may be any length). */
+#define MLA_TREE_MAX_NODES 1024
+
+/* Plan one step of drafted trees: mla_plan (causal) with
+ *   parents  host int32 [qo_indptr[batch]]: in [-1, i) for node i of a row
+ * Every row needs k_b >= q_b (its nodes have cache slots), and a row that is not a chain
+ * at most MLA_TREE_MAX_NODES nodes.  Graph buckets, split keys and the cascade apply (a
+ * shared prefix then ends with the rows' context); context_only is refused.  mla_run,
+ * mla_append_kv and mla_run_append take the plan as any other.  Where a masked node's
+ * latent row holds an infinity or a NaN, the nodes that do not see it are unaffected.
+ * Errors: as mla_plan, and INVALID_ARGUMENT for bad parents, a row with k_b < q_b, a
+ * larger tree, or context_only. */
+mla_status mla_plan_tree(const mla_dims* dims, int32_t batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
+                         const int32_t* kv_indices, const int32_t* last_page_len, const int32_t* parents,
+                         void* stream, const mla_plan_options* opts, mla_plan_t* out_plan);
+
+/* mla_plan_update for a plan made by mla_plan_tree (the two are not interchangeable: each
+ * refuses the other's plans with INVALID_ARGUMENT).  The step is unchanged, and *reused 1,
+ * when the tables and the parents equal those of the plan's current step. */
+mla_status mla_plan_tree_update(mla_plan_t plan, int32_t batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
+                                const int32_t* kv_indices, const int32_t* last_page_len, const int32_t* parents,
+                                void* stream, int32_t* reused);
+
+/* Copy a tree plan's bookkeeping to host arrays (each may be NULL):
+ *   items [num_work * MLA_TREE_ITEM_FIELDS] beside mla_plan_describe's work records:
+ *     { word_base, words, first_tile, 0 }: query token i of the item's tile (its rows
+ *     [i * H, (i + 1) * H)) sees key 64 * (first_tile + w) + bit of its row where that bit
+ *     of words[word_base + i * words + w] is set, and every key below 64 * first_tile;
+ *     words == 0: the item's rows are chains (work's diag_base says all)
+ *   nodes [T * MLA_TREE_NODE_FIELDS] { parent, first_child, next_sibling, row }: indices
+ *     within the row, -1 for none; children are in increasing order
+ *   words [*num_words], the mask words; pass NULL to learn *num_words (may be NULL)
+ * Errors: INVALID_ARGUMENT (NULL, or not a tree plan). */
+#define MLA_TREE_ITEM_FIELDS 4
+#define MLA_TREE_NODE_FIELDS 4
+mla_status mla_plan_describe_tree(mla_plan_t plan, int32_t* items, int32_t* nodes, uint64_t* words,
+                                  int64_t* num_words);
+
+/* Element types of the probabilities given to mla_verify_tree. */
+typedef enum { MLA_PROB_FP32 = 0, MLA_PROB_BF16 = 1 } mla_prob_type;
+
+/* Verify a step's drafted trees against the target's probabilities, from given random
+ * numbers: the tokens that result are distributed as the target's own (recursive
+ * rejection along the tree).  Row b's walk starts at its node 0, the row's last decided
+ * token (other roots are never reached).  With p and q the target's and the draft's
+ * weights at node v, w = p and Z = 1, the children c of v are tried in order:
+ *     x = draft_tokens[c];  accepted if  uniform[c] * q(x) * Z < w(x)
+ *     else, before the next child:  w = max(w - Z q, 0),  Z = sum of w
+ * and an accepted child is the next v.  Where every child was rejected (or v has none),
+ * w as the rejections left it (p where that is zero everywhere) gives the next token: the
+ * first x whose running sum of w exceeds uniform_next[b] * (sum of w).
+ * Without draft_probs the drafted tokens are point masses: a child is accepted if
+ * uniform[c] * Z < w(x), else w(x) = 0 and Z = max(Z - w(x), 0).
+ * A draft token < 0 was given, not drafted: it is accepted without a test.  One >= vocab
+ * has weight 0.  Weights that are negative, infinite or NaN count as 0.  All sums and
+ * comparisons are in 64 bits, in an order that does not change from call to call.
+ *   vocab         in [1, 2^28]
+ *   draft_tokens  device int32 [T]; node 0's is not read
+ *   target_probs  device [T] rows of `vocab` weights, row pitch ld_target (elements, >=
+ *                 vocab): row t is the target's distribution AFTER token t
+ *   draft_probs   the same of the draft, pitch ld_draft: row t is the distribution that
+ *                 t's children were drawn from; or NULL (point masses)
+ *   prob_type     of both
+ *   uniform       device fp32 [T] in [0, 1): token t's is used when t is tried
+ *   uniform_next  device fp32 [batch] in [0, 1)
+ *   accept_index  device int32 [T] (written): row b's first num_accepted[b] entries are the
+ *                 accepted path's nodes (indices within the row, 0 first), the rest -1
+ *   num_accepted  device int32 [batch] (written): nodes of the path, the root included; 0
+ *                 for a row without tokens
+ *   next_token    device int32 [batch] (written): -1 for a row without tokens, or where no
+ *                 weight is positive
+ * For a graph plan T and batch are the bucket's bounds; entries behind the step's rows and
+ * tokens are neither read nor written.  A row of more than MLA_TREE_MAX_NODES tokens is
+ * refused with UNSUPPORTED (a graph replay, which is not checked, gives it num_accepted 0
+ * and next_token -1).  One launch, no allocation, no synchronisation.
+ * Errors: INVALID_ARGUMENT (NULL or misaligned pointer, vocab or pitch, not a tree plan),
+ * UNSUPPORTED, CUDA. */
+mla_status mla_verify_tree(mla_plan_t plan, const int32_t* draft_tokens, const void* target_probs, int64_t ld_target,
+                           const void* draft_probs, int64_t ld_draft, int32_t vocab, mla_prob_type prob_type,
+                           const float* uniform, const float* uniform_next, int32_t* accept_index,
+                           int32_t* num_accepted, int32_t* next_token, void* stream);
+
+/* Move the accepted nodes' latent rows to consecutive cache slots, in place, in every
+ * layer's cache: entry k of row b's path (node a = accept_index[qo_indptr[b] + k], k <
+ * num_accepted[b]) goes from key c_b + a to key c_b + k.  The row then holds c_b +
+ * num_accepted[b] keys; its slots behind those are free.
+ *   accept_index, num_accepted  device int32, as mla_verify_tree writes them (for each row
+ *                 the entries increase); an entry outside [k, q_b) moves nothing
+ *   caches        host array of num_caches device pointers, each bf16
+ *                 [num_pages][page_size][512 + rope_dim], none overlapping another
+ * One launch per 128 caches, no allocation, no synchronisation.
+ * Errors: INVALID_ARGUMENT (NULL or misaligned pointer, overlapping caches, not a tree plan, or two
+ * of the step's tokens name one cache slot), CUDA. */
+mla_status mla_compact_kv(mla_plan_t plan, const int32_t* accept_index, const int32_t* num_accepted,
+                          void* const* caches, int32_t num_caches, void* stream);
+
+/* Copy cache pages, in every layer's cache: the first num_tokens[i] tokens of page
+ * src_pages[i] to page dst_pages[i].  Forking a sequence shares its full pages by naming
+ * them twice and copies the page that both would write; compacting a pool moves live
+ * pages to free ones.
+ *   dims          the cache's geometry (num_heads and sm_scale are not used, but checked)
+ *   src_pages, dst_pages  host int32 [num_pairs], in [0, num_pages); a source may be
+ *                 repeated, a destination may not, nor be a source of any pair
+ *   num_tokens    host int32 [num_pairs], in [0, page_size]; NULL: whole pages
+ *   caches        as for mla_compact_kv
+ * The host arrays are read during the call and travel as kernel arguments, so the call can
+ * be captured into a CUDA graph (which then repeats these pairs).  One launch per 1024
+ * pairs and 128 caches, no device allocation, no synchronisation.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (shape), OUT_OF_MEMORY (host), CUDA. */
+mla_status mla_copy_pages(const mla_dims* dims, const int32_t* src_pages, const int32_t* dst_pages,
+                          const int32_t* num_tokens, int32_t num_pairs, void* const* caches, int32_t num_caches,
+                          void* stream);
+
 /* Wait for the plan's last run, then free everything it owns.  NULL is a no-op. */
 void mla_plan_destroy(mla_plan_t plan);
 

@@ -9,7 +9,8 @@ Names follow the C ABI in ``include/mla.h``: ``mla_supports``, ``mla_plan``,
 ``mla_plan_update``, ``mla_run``, ``mla_append_kv``, ``mla_run_append``,
 ``mla_merge_state``, ``mla_plan_check``, ``mla_plan_get_info``, ``mla_plan_describe``,
 ``mla_plan_kernel_times``, ``mla_run_noalloc``, ``mla_plan_destroy``,
-``mla_status_string``.
+``mla_status_string``; for speculative steps ``mla_plan_tree``, ``mla_plan_tree_update``,
+``mla_plan_describe_tree``, ``mla_verify_tree``, ``mla_compact_kv``, ``mla_copy_pages``.
 """
 
 from __future__ import annotations
@@ -34,6 +35,10 @@ MLA_DEBUG_DROP_FIRST_KV_LOAD = 1
 MLA_DEBUG_KERNEL_TIMING = 2
 WORK_FIELDS = 8
 MERGE_FIELDS = 4
+TREE_FIELDS = 4  # of a tree item and of a tree node
+MLA_TREE_MAX_NODES = 1024
+MLA_PROB_FP32 = 0
+MLA_PROB_BF16 = 1
 KV_LORA_RANK = 512
 ROPE_DIM = 64
 
@@ -50,6 +55,12 @@ EXPORTED = (
     "mla_plan_describe",
     "mla_plan_kernel_times",
     "mla_run_noalloc",
+    "mla_plan_tree",
+    "mla_plan_tree_update",
+    "mla_plan_describe_tree",
+    "mla_verify_tree",
+    "mla_compact_kv",
+    "mla_copy_pages",
     "mla_plan_destroy",
     "mla_status_string",
 )
@@ -145,6 +156,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mla_run_noalloc.argtypes = [ctypes.POINTER(_Dims), ctypes.c_int32, i32p, i32p, i32p, i32p, ctypes.c_int32,
                                     vp, vp, vp, vp, vp, vp, vp]
     lib.mla_run_noalloc.restype = ctypes.c_int
+    lib.mla_plan_tree.argtypes = [ctypes.POINTER(_Dims), ctypes.c_int32, i32p, i32p, i32p, i32p, i32p, vp,
+                                  ctypes.POINTER(_Options), ctypes.POINTER(vp)]
+    lib.mla_plan_tree.restype = ctypes.c_int
+    lib.mla_plan_tree_update.argtypes = [vp, ctypes.c_int32, i32p, i32p, i32p, i32p, i32p, vp, i32p]
+    lib.mla_plan_tree_update.restype = ctypes.c_int
+    lib.mla_plan_describe_tree.argtypes = [vp, i32p, i32p, vp, vp]
+    lib.mla_plan_describe_tree.restype = ctypes.c_int
+    lib.mla_verify_tree.argtypes = [vp, vp, vp, ctypes.c_int64, vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, vp,
+                                    vp, vp, vp, vp, vp]
+    lib.mla_verify_tree.restype = ctypes.c_int
+    lib.mla_compact_kv.argtypes = [vp, vp, vp, vp, ctypes.c_int32, vp]
+    lib.mla_compact_kv.restype = ctypes.c_int
+    lib.mla_copy_pages.argtypes = [ctypes.POINTER(_Dims), i32p, i32p, i32p, ctypes.c_int32, vp, ctypes.c_int32, vp]
+    lib.mla_copy_pages.restype = ctypes.c_int
     lib.mla_plan_destroy.argtypes = [vp]
     lib.mla_plan_destroy.restype = None
     lib.mla_status_string.argtypes = [ctypes.c_int]
@@ -188,7 +213,7 @@ class MlaPlan:
     """Owns one C plan handle (``mla_plan_t``); destroyed with the object."""
 
     def __init__(self, handle: int, batch: int, num_heads: int, total_tokens: int, graph_max_tokens: int = 0,
-                 rope_dim: int = ROPE_DIM, num_pages: int = 0, page_size: int = 0):
+                 rope_dim: int = ROPE_DIM, num_pages: int = 0, page_size: int = 0, graph_max_batch: int = 0):
         self._h = ctypes.c_void_p(handle)
         self.batch = batch
         self.num_heads = num_heads
@@ -199,6 +224,12 @@ class MlaPlan:
         self.page_size = page_size
         # a graph plan's per-token buffers hold graph_max_tokens tokens
         self.graph_max_tokens = graph_max_tokens
+        self.graph_max_batch = graph_max_batch
+
+    @property
+    def batch_capacity(self) -> int:
+        """Rows every per-row buffer passed with this plan must hold."""
+        return self.graph_max_batch if self.graph_max_tokens > 0 else self.batch
 
     @property
     def token_capacity(self) -> int:
@@ -223,6 +254,40 @@ class MlaPlan:
             pass
 
 
+def _step_tables(who, qo_indptr, kv_indptr, kv_indices, last_page_len):
+    """A step's tables as host int32 arrays that the library can read."""
+    qo = _i32(qo_indptr)
+    kvp = _i32(kv_indptr)
+    kvi = _i32(kv_indices)
+    last = _i32(last_page_len)
+    batch = len(qo) - 1
+    if batch < 0 or len(kvp) != batch + 1 or len(last) != batch:
+        raise MlaError(MLA_ERR_INVALID_ARGUMENT, f"{who}: table lengths")
+    if len(kvi) < int(kvp[-1]):
+        raise MlaError(MLA_ERR_INVALID_ARGUMENT, f"{who}: kv_indices shorter than kv_indptr[-1]")
+    kvi = kvi if len(kvi) else np.zeros(1, dtype=np.int32)
+    last = last if len(last) else np.zeros(1, dtype=np.int32)
+    return qo, kvp, kvi, last
+
+
+def _make_plan(who, tables, extra, dims, opts, stream) -> MlaPlan:
+    """Call the plan-making entry ``who``; ``extra`` is its argument after the tables."""
+    qo, kvp, kvi, last = tables
+    batch = len(qo) - 1
+    if stream is None and not opts.host_only:
+        import torch
+
+        stream = torch.cuda.current_stream().cuda_stream
+    out = ctypes.c_void_p()
+    st = getattr(load_library(), who)(ctypes.byref(dims), batch, _ptr(qo), _ptr(kvp), _ptr(kvi), _ptr(last), extra,
+                                      ctypes.c_void_p(stream or 0), ctypes.byref(opts), ctypes.byref(out))
+    if st != MLA_OK:
+        raise MlaError(st, who)
+    graph = opts.graph_max_tokens > 0
+    return MlaPlan(out.value, batch, dims.num_heads, int(qo[-1]), opts.graph_max_tokens if graph else 0,
+                   dims.rope_dim, dims.num_pages, dims.page_size, opts.graph_max_batch if graph else 0)
+
+
 def mla_plan(qo_indptr, kv_indptr, kv_indices, last_page_len, *, num_heads: int, page_size: int, num_pages: int,
              sm_scale: float, causal: bool = True, kv_lora_rank: int = KV_LORA_RANK, rope_dim: int = ROPE_DIM,
              split_keys: int = 0, num_sms: int = 0, wait_timeout_ns: int = 0, debug_flags: int = 0,
@@ -233,31 +298,11 @@ def mla_plan(qo_indptr, kv_indptr, kv_indices, last_page_len, *, num_heads: int,
     plan for a bucket (fixed device buffers and launch shapes, re-planned in place by
     ``mla_plan_update``); ``context_only`` attends only each row's stored context;
     ``cascade`` attends prefixes shared by consecutive rows once per group."""
-    lib = load_library()
-    qo = _i32(qo_indptr)
-    kvp = _i32(kv_indptr)
-    kvi = _i32(kv_indices)
-    last = _i32(last_page_len)
-    batch = len(qo) - 1
-    if batch < 0 or len(kvp) != batch + 1 or len(last) != batch:
-        raise MlaError(MLA_ERR_INVALID_ARGUMENT, "mla_plan: table lengths")
-    if len(kvi) < int(kvp[-1]):
-        raise MlaError(MLA_ERR_INVALID_ARGUMENT, "mla_plan: kv_indices shorter than kv_indptr[-1]")
+    tables = _step_tables("mla_plan", qo_indptr, kv_indptr, kv_indices, last_page_len)
     dims = _Dims(num_heads, kv_lora_rank, rope_dim, page_size, num_pages, sm_scale)
     opts = _Options(split_keys, num_sms, wait_timeout_ns, debug_flags, 1 if host_only else 0, graph_max_batch,
                     graph_max_tokens, graph_max_page_ids, 1 if context_only else 0, 1 if cascade else 0)
-    if stream is None and not host_only:
-        import torch
-
-        stream = torch.cuda.current_stream().cuda_stream
-    out = ctypes.c_void_p()
-    kvi_arr = kvi if len(kvi) else np.zeros(1, dtype=np.int32)
-    st = lib.mla_plan(ctypes.byref(dims), batch, _ptr(qo), _ptr(kvp), _ptr(kvi_arr), _ptr(last),
-                      1 if causal else 0, ctypes.c_void_p(stream or 0), ctypes.byref(opts), ctypes.byref(out))
-    if st != MLA_OK:
-        raise MlaError(st, "mla_plan")
-    return MlaPlan(out.value, batch, num_heads, int(qo[-1]), graph_max_tokens if graph_max_tokens > 0 else 0,
-                   rope_dim, num_pages, page_size)
+    return _make_plan("mla_plan", tables, 1 if causal else 0, dims, opts, stream)
 
 
 def mla_plan_update(plan: MlaPlan, qo_indptr, kv_indptr, kv_indices, last_page_len, stream=None) -> bool:
@@ -487,6 +532,208 @@ def mla_run_noalloc(qo_indptr, kv_indptr, kv_indices, last_page_len, q_nope, q_p
         ctypes.c_void_p(stream or 0), ctypes.c_void_p(status.data_ptr() if status is not None else 0))
     if st != MLA_OK:
         raise MlaError(st, "mla_run_noalloc")
+
+
+def _tree_parents(who, parents, qo) -> np.ndarray:
+    par = _i32(parents)
+    if par.ndim != 1 or len(par) != max(0, int(qo[-1])):
+        raise MlaError(MLA_ERR_INVALID_ARGUMENT, f"{who}: parents must have qo_indptr[-1] entries")
+    return par if len(par) else np.zeros(1, dtype=np.int32)
+
+
+def mla_plan_tree(qo_indptr, kv_indptr, kv_indices, last_page_len, parents, *, num_heads: int, page_size: int,
+                  num_pages: int, sm_scale: float, kv_lora_rank: int = KV_LORA_RANK, rope_dim: int = ROPE_DIM,
+                  split_keys: int = 0, num_sms: int = 0, wait_timeout_ns: int = 0, debug_flags: int = 0,
+                  host_only: bool = False, graph_max_batch: int = 0, graph_max_tokens: int = 0,
+                  graph_max_page_ids: int = 0, context_only: bool = False, cascade: bool = False,
+                  stream=None) -> MlaPlan:
+    """Plan one step whose rows draft trees of tokens (``mla_plan_tree``): ``parents`` (host
+    int32, one per token) is the index within the row of the node a token continues, or -1.
+    A token attends its row's context, its ancestors and itself.  The plan is run with
+    ``mla_run`` and re-planned in place with ``mla_plan_tree_update``; other arguments as
+    for ``mla_plan``."""
+    tables = _step_tables("mla_plan_tree", qo_indptr, kv_indptr, kv_indices, last_page_len)
+    par = _tree_parents("mla_plan_tree", parents, tables[0])
+    dims = _Dims(num_heads, kv_lora_rank, rope_dim, page_size, num_pages, sm_scale)
+    opts = _Options(split_keys, num_sms, wait_timeout_ns, debug_flags, 1 if host_only else 0, graph_max_batch,
+                    graph_max_tokens, graph_max_page_ids, 1 if context_only else 0, 1 if cascade else 0)
+    return _make_plan("mla_plan_tree", tables, _ptr(par), dims, opts, stream)
+
+
+def mla_plan_tree_update(plan: MlaPlan, qo_indptr, kv_indptr, kv_indices, last_page_len, parents,
+                         stream=None) -> bool:
+    """Re-plan a tree plan in place for another step (``mla_plan_tree_update``).  Returns
+    True when the tables and the parents equal those of the plan's current step."""
+    qo, kvp, kvi, last = _step_tables("mla_plan_tree_update", qo_indptr, kv_indptr, kv_indices, last_page_len)
+    par = _tree_parents("mla_plan_tree_update", parents, qo)
+    if stream is None:
+        import torch
+
+        stream = torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
+    batch = len(qo) - 1
+    reused = ctypes.c_int32(0)
+    st = load_library().mla_plan_tree_update(plan.handle, batch, _ptr(qo), _ptr(kvp), _ptr(kvi), _ptr(last), _ptr(par),
+                                             ctypes.c_void_p(stream or 0), ctypes.addressof(reused))
+    if st != MLA_OK:
+        raise MlaError(st, "mla_plan_tree_update")
+    plan.batch = batch
+    plan.total_tokens = int(qo[-1])
+    return bool(reused.value)
+
+
+def mla_plan_describe_tree(plan: MlaPlan) -> dict:
+    """items [num_work, 4], nodes [T, 4] (int32) and mask words [n] (uint64) of a tree plan."""
+    info = mla_plan_get_info(plan)
+    lib = load_library()
+    n = ctypes.c_int64(0)
+    st = lib.mla_plan_describe_tree(plan.handle, None, None, None, ctypes.addressof(n))
+    if st != MLA_OK:
+        raise MlaError(st, "mla_plan_describe_tree")
+    items = np.zeros((max(1, info["num_work"]), TREE_FIELDS), dtype=np.int32)
+    nodes = np.zeros((max(1, info["total_tokens"]), TREE_FIELDS), dtype=np.int32)
+    words = np.zeros(max(1, n.value), dtype=np.uint64)
+    st = lib.mla_plan_describe_tree(plan.handle, _ptr(items), _ptr(nodes), _ptr(words), None)
+    if st != MLA_OK:
+        raise MlaError(st, "mla_plan_describe_tree")
+    return {"items": items[: info["num_work"]], "nodes": nodes[: info["total_tokens"]], "words": words[: n.value]}
+
+
+def _check_current_device(*tensors) -> None:
+    import torch
+
+    for t in tensors:
+        if t is not None and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors must be on the current device, got {t.device}")
+
+
+def _check_rows(t, name, dtype, tokens: int, vocab: int):
+    """A [tokens, vocab] CUDA tensor whose rows are contiguous (any row pitch)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (tokens, vocab):
+        raise ValueError(f"{name} must have shape {(tokens, vocab)}, got {tuple(t.shape)}")
+    if vocab > 1 and t.stride(1) != 1 or tokens > 1 and t.stride(0) < vocab:
+        raise ValueError(f"{name} must have contiguous rows")
+
+
+def mla_verify_tree(plan: MlaPlan, draft_tokens, target_probs, uniform, uniform_next, draft_probs=None,
+                    accept_index=None, num_accepted=None, next_token=None, stream=None):
+    """Verify a tree plan's drafted tokens against the target's probabilities, from given
+    random numbers (``mla_verify_tree``).  ``target_probs`` and ``draft_probs`` (None:
+    point masses) are [T, vocab] fp32 or bf16 with contiguous rows; ``draft_tokens`` [T]
+    int32; ``uniform`` [T] and ``uniform_next`` [batch] fp32.  Returns (accept_index [T],
+    num_accepted [batch], next_token [batch]), int32."""
+    import torch
+
+    T, B = plan.token_capacity, plan.batch_capacity
+    if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2 or target_probs.shape[1] < 1:
+        raise ValueError("target_probs must be a [T, vocab] tensor")
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"target_probs must be float32 or bfloat16, got {target_probs.dtype}")
+    V, kind, dev = target_probs.shape[1], target_probs.dtype, target_probs.device
+    _check_rows(target_probs, "target_probs", kind, T, V)
+    if draft_probs is not None:
+        _check_rows(draft_probs, "draft_probs", kind, T, V)
+    _check_dev_tensor(draft_tokens, "draft_tokens", torch.int32, (T,))
+    _check_dev_tensor(uniform, "uniform", torch.float32, (T,))
+    _check_dev_tensor(uniform_next, "uniform_next", torch.float32, (B,))
+    if accept_index is None:
+        accept_index = torch.empty(T, dtype=torch.int32, device=dev)
+    if num_accepted is None:
+        num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    if next_token is None:
+        next_token = torch.empty(B, dtype=torch.int32, device=dev)
+    _check_dev_tensor(accept_index, "accept_index", torch.int32, (T,))
+    _check_dev_tensor(num_accepted, "num_accepted", torch.int32, (B,))
+    _check_dev_tensor(next_token, "next_token", torch.int32, (B,))
+    _check_current_device(target_probs, draft_probs, draft_tokens, uniform, uniform_next, accept_index, num_accepted,
+                          next_token)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+
+    def pitch(t):
+        return max(V, t.stride(0)) if T > 1 else V
+
+    vp = ctypes.c_void_p
+    st = load_library().mla_verify_tree(
+        plan.handle, vp(draft_tokens.data_ptr()), vp(target_probs.data_ptr()), pitch(target_probs),
+        vp(draft_probs.data_ptr() if draft_probs is not None else 0),
+        pitch(draft_probs) if draft_probs is not None else 0, V,
+        MLA_PROB_FP32 if kind == torch.float32 else MLA_PROB_BF16, vp(uniform.data_ptr()),
+        vp(uniform_next.data_ptr()), vp(accept_index.data_ptr()), vp(num_accepted.data_ptr()),
+        vp(next_token.data_ptr()), vp(stream or 0))
+    if st != MLA_OK:
+        raise MlaError(st, "mla_verify_tree")
+    return accept_index, num_accepted, next_token
+
+
+def _cache_list(caches):
+    """The layers' caches of one call: a list of tensors [num_pages, page_size, width], or
+    one tensor with a leading layer dimension (or none, for a single layer)."""
+    import torch
+
+    if isinstance(caches, torch.Tensor):
+        caches = list(caches.unbind(0)) if caches.dim() == 4 else [caches]
+    return list(caches)
+
+
+def mla_compact_kv(plan: MlaPlan, accept_index, num_accepted, caches, stream=None) -> None:
+    """Move the accepted nodes' latent rows to consecutive cache slots in every layer's
+    cache, in place (``mla_compact_kv``).  ``caches``: a list of [num_pages, page_size,
+    512 + rope_dim] tensors, or one tensor with a leading layer dimension."""
+    import torch
+
+    caches = _cache_list(caches)
+    width = KV_LORA_RANK + plan.rope_dim
+    for c in caches:
+        _check_cache_shape(c, plan.num_pages, plan.page_size, plan.rope_dim)
+        _check_dev_tensor(c, "cache", torch.bfloat16, (c.shape[0], plan.page_size, width))
+    _check_dev_tensor(accept_index, "accept_index", torch.int32, (plan.token_capacity,))
+    _check_dev_tensor(num_accepted, "num_accepted", torch.int32, (plan.batch_capacity,))
+    _check_current_device(accept_index, num_accepted, *caches)
+    if stream is None:
+        stream = torch.cuda.current_stream(accept_index.device).cuda_stream
+    ptrs = (ctypes.c_void_p * max(1, len(caches)))(*[c.data_ptr() for c in caches])
+    st = load_library().mla_compact_kv(plan.handle, ctypes.c_void_p(accept_index.data_ptr()),
+                                       ctypes.c_void_p(num_accepted.data_ptr()), ptrs, len(caches),
+                                       ctypes.c_void_p(stream or 0))
+    if st != MLA_OK:
+        raise MlaError(st, "mla_compact_kv")
+
+
+def mla_copy_pages(src_pages, dst_pages, caches, num_tokens=None, stream=None) -> None:
+    """Copy the first ``num_tokens[i]`` tokens (None: all) of page ``src_pages[i]`` to page
+    ``dst_pages[i]`` in every layer's cache (``mla_copy_pages``).  The tables are host
+    arrays; ``caches`` as for ``mla_compact_kv``, all of one shape and on the current
+    device."""
+    import torch
+
+    caches = _cache_list(caches)
+    src, dst = _i32(src_pages), _i32(dst_pages)
+    tok = None if num_tokens is None else _i32(num_tokens)
+    if src.ndim != 1 or dst.shape != src.shape or (tok is not None and tok.shape != src.shape):
+        raise MlaError(MLA_ERR_INVALID_ARGUMENT, "mla_copy_pages: table lengths")
+    if not caches:
+        return
+    shape = tuple(getattr(caches[0], "shape", ()))
+    if len(shape) != 3:
+        raise ValueError("caches must be [num_pages, page_size, 512 + rope_dim]")
+    for c in caches:
+        _check_dev_tensor(c, "cache", torch.bfloat16, shape)
+    _check_current_device(*caches)
+    if stream is None:
+        stream = torch.cuda.current_stream(caches[0].device).cuda_stream
+    dims = _Dims(128, KV_LORA_RANK, shape[2] - KV_LORA_RANK, shape[1], shape[0], 1.0)
+    ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+    st = load_library().mla_copy_pages(ctypes.byref(dims), _ptr(src), _ptr(dst),
+                                       None if tok is None else _ptr(tok), len(src), ptrs, len(caches),
+                                       ctypes.c_void_p(stream or 0))
+    if st != MLA_OK:
+        raise MlaError(st, "mla_copy_pages")
 
 
 def mla_plan_check(plan: MlaPlan) -> int:

@@ -3,11 +3,14 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <limits>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <utility>
@@ -28,15 +31,19 @@ struct mla_plan_s {
   PlanLayout spare;  // the previous step's layout, kept so a re-plan reuses its capacity
   int device = -1;
   bool host_only = false;
+  bool tree = false;      // made by mla_plan_tree
   bool graph = false;     // fixed buffers and launch shapes (opts.graph_max_*)
   bool captured = false;  // mla_run was called on a capturing stream
   // the step's tables, to recognise an unchanged step in mla_plan_update
-  std::vector<int32_t> fp_qo, fp_kvp, fp_kvi, fp_last;
+  std::vector<int32_t> fp_qo, fp_kvp, fp_kvi, fp_last, fp_parents;
   // capacities of the device lists (exact sizes unless a graph plan) and the layout of
-  // the device blob: [status (256 B)] [work] [merge] [refs] [append rows] [kv_indices]
+  // the device blob: [status (256 B)] [work] [merge] [refs] [append rows] [kv_indices] and,
+  // for a tree plan, [tree items] [tree rows] [tree nodes] [mask words]
   struct Sizes {
     int64_t cap_work = 0, cap_merge = 0, cap_refs = 0, cap_tokens = 0, cap_idx = 0, cap_ws_rows = 0;
-    size_t off_work = 0, off_merge = 0, off_refs = 0, off_append = 0, off_idx = 0, blob_bytes = 0;
+    int64_t cap_rows = 0, cap_words = 0;  // tree plans
+    size_t off_work = 0, off_merge = 0, off_refs = 0, off_append = 0, off_idx = 0;
+    size_t off_titems = 0, off_trows = 0, off_tnodes = 0, off_twords = 0, blob_bytes = 0;
   } sz;
   void* d_blob = nullptr;
   bool blob_fresh = false;  // the blob's status word has not been cleared yet
@@ -66,6 +73,10 @@ struct mla_plan_s {
   }
   const int32_t* d_kv_indices() const {
     return reinterpret_cast<const int32_t*>(static_cast<uint8_t*>(d_blob) + sz.off_idx);
+  }
+  template <typename T>
+  const T* d_tree(size_t off) const {
+    return reinterpret_cast<const T*>(static_cast<uint8_t*>(d_blob) + off);
   }
 };
 
@@ -265,7 +276,7 @@ void free_plan(mla_plan_s* p) {
 
 // The request a plan's options describe, for its current tables.
 PlanRequest request_of(const mla_plan_s* p, int32_t batch, const int32_t* qo, const int32_t* kvp, const int32_t* kvi,
-                       const int32_t* last) {
+                       const int32_t* last, const int32_t* parents) {
   PlanRequest r;
   r.d = p->dims;
   r.batch = batch;
@@ -276,6 +287,8 @@ PlanRequest request_of(const mla_plan_s* p, int32_t batch, const int32_t* qo, co
   r.causal = p->causal;
   r.context_only = p->opts.context_only != 0;
   r.cascade = p->opts.cascade != 0;
+  r.tree = p->tree;
+  r.parents = parents;
   r.split_keys = p->opts.split_keys;
   r.num_sms = p->opts.num_sms;
   if (p->graph)
@@ -291,7 +304,11 @@ bool fits_bucket(const mla_plan_s* p, int32_t batch, const int32_t* qo, const in
 }
 
 // Device list capacities and blob offsets: exact sizes, or the bucket's bounds.
-void size_lists(mla_plan_s* p, const PlanLayout& L, int64_t n_idx) {
+void size_lists(mla_plan_s* p, const PlanLayout& L, int32_t batch, int64_t n_idx) {
+  if (p->tree) {
+    p->sz.cap_rows = p->graph ? p->opts.graph_max_batch : batch;
+    p->sz.cap_words = p->graph ? tree_words_bound(p->opts.graph_max_tokens) : static_cast<int64_t>(L.tree_words.size());
+  }
   if (p->graph) {
     PlanRequest r;
     graph_bounds(p->dims.num_heads, p->opts.graph_max_batch, p->opts.graph_max_tokens, p->opts.num_sms, &r);
@@ -315,6 +332,13 @@ void size_lists(mla_plan_s* p, const PlanLayout& L, int64_t n_idx) {
   p->sz.off_append = align_up(p->sz.off_refs + sizeof(int32_t) * p->sz.cap_refs, 256);
   p->sz.off_idx = align_up(p->sz.off_append + sizeof(int32_t) * p->sz.cap_tokens, 256);
   p->sz.blob_bytes = align_up(p->sz.off_idx + sizeof(int32_t) * p->sz.cap_idx, 256);
+  if (p->tree) {
+    p->sz.off_titems = p->sz.blob_bytes;
+    p->sz.off_trows = align_up(p->sz.off_titems + sizeof(TreeItem) * p->sz.cap_work, 256);
+    p->sz.off_tnodes = align_up(p->sz.off_trows + sizeof(TreeRow) * p->sz.cap_rows, 256);
+    p->sz.off_twords = align_up(p->sz.off_tnodes + sizeof(TreeNode) * p->sz.cap_tokens, 256);
+    p->sz.blob_bytes = align_up(p->sz.off_twords + sizeof(uint64_t) * p->sz.cap_words, 256);
+  }
 }
 
 // Make sure the pooled device buffers hold the current capacities.  Growing a buffer
@@ -348,7 +372,7 @@ mla_status reserve_device(mla_plan_s* p) {
 
 // Stage the current layout and page table in pinned memory and enqueue their upload
 // (everything after the status word).  Unused capacity of a graph plan is filled with
-// empty work and merge items and append rows of -1.
+// empty work and merge items, append rows of -1 and tree rows of -1 nodes.
 mla_status upload(mla_plan_s* p, const int32_t* kv_indices, int64_t n_idx, cudaStream_t s) {
   const int k = static_cast<int>(p->uploads & 1);
   if (p->upload_pending[k]) {
@@ -374,12 +398,25 @@ mla_status upload(mla_plan_s* p, const int32_t* kv_indices, int64_t n_idx, cudaS
   for (int64_t t = 0; t < p->sz.cap_tokens; ++t)
     app[t] = t < static_cast<int64_t>(L.append_rows.size()) ? L.append_rows[t] : -1;
   if (n_idx > 0) std::memcpy(h + p->sz.off_idx, kv_indices, sizeof(int32_t) * n_idx);
+  if (p->tree) {
+    auto put = [h](size_t off, const void* src, size_t bytes) {
+      if (bytes > 0) std::memcpy(h + off, src, bytes);
+    };
+    put(p->sz.off_titems, L.tree_items.data(), sizeof(TreeItem) * L.tree_items.size());
+    put(p->sz.off_trows, L.tree_rows.data(), sizeof(TreeRow) * L.tree_rows.size());
+    TreeRow* rows = reinterpret_cast<TreeRow*>(h + p->sz.off_trows);
+    for (int64_t b = static_cast<int64_t>(L.tree_rows.size()); b < p->sz.cap_rows; ++b) rows[b] = TreeRow{0, -1};
+    put(p->sz.off_tnodes, L.tree_nodes.data(), sizeof(TreeNode) * L.tree_nodes.size());
+    put(p->sz.off_twords, L.tree_words.data(), sizeof(uint64_t) * L.tree_words.size());
+  }
   // a fresh blob's status word is cleared by the same copy; later uploads leave it alone
   // (a run still in flight may be reporting a timeout there)
   const size_t from = p->blob_fresh ? 0 : p->sz.off_work;
   if (p->blob_fresh) std::memset(h, 0, p->sz.off_work);
+  // the mask words are last, and only the step's are read
+  const size_t to = p->tree ? p->sz.off_twords + sizeof(uint64_t) * L.tree_words.size() : p->sz.blob_bytes;
   uint8_t* d = static_cast<uint8_t*>(p->d_blob);
-  if (cudaMemcpyAsync(d + from, h + from, p->sz.blob_bytes - from, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+  if (cudaMemcpyAsync(d + from, h + from, to - from, cudaMemcpyHostToDevice, s) != cudaSuccess ||
       cudaEventRecord(p->ev_upload[k], s) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
@@ -391,7 +428,7 @@ mla_status upload(mla_plan_s* p, const int32_t* kv_indices, int64_t n_idx, cudaS
 }
 
 void remember_tables(mla_plan_s* p, int32_t batch, const int32_t* qo, const int32_t* kvp, const int32_t* kvi,
-                     const int32_t* last) {
+                     const int32_t* last, const int32_t* parents) {
   p->batch = batch;
   p->fp_qo.assign(qo, qo + batch + 1);
   p->fp_kvp.assign(kvp, kvp + batch + 1);
@@ -404,10 +441,23 @@ void remember_tables(mla_plan_s* p, int32_t batch, const int32_t* qo, const int3
     p->fp_last.assign(last, last + batch);
   else
     p->fp_last.clear();
+  if (p->tree && qo[batch] > 0)
+    p->fp_parents.assign(parents, parents + qo[batch]);
+  else
+    p->fp_parents.clear();
+}
+
+// Make room for a step's tables, so that remember_tables cannot fail half way.
+void reserve_tables(mla_plan_s* p, int32_t batch, const int32_t* qo, const int32_t* kvp) {
+  p->fp_qo.reserve(batch + 1);
+  p->fp_kvp.reserve(batch + 1);
+  p->fp_kvi.reserve(batch > 0 ? kvp[batch] : 0);
+  p->fp_last.reserve(batch);
+  if (p->tree) p->fp_parents.reserve(qo[batch]);
 }
 
 bool same_tables(const mla_plan_s* p, int32_t batch, const int32_t* qo, const int32_t* kvp, const int32_t* kvi,
-                 const int32_t* last) {
+                 const int32_t* last, const int32_t* parents) {
   if (batch != p->batch || batch < 0 || !qo || !kvp) return false;
   if (std::memcmp(qo, p->fp_qo.data(), sizeof(int32_t) * (batch + 1)) != 0) return false;
   if (std::memcmp(kvp, p->fp_kvp.data(), sizeof(int32_t) * (batch + 1)) != 0) return false;
@@ -415,6 +465,9 @@ bool same_tables(const mla_plan_s* p, int32_t batch, const int32_t* qo, const in
   const int32_t n_idx = batch > 0 ? kvp[batch] : 0;
   if (n_idx != static_cast<int32_t>(p->fp_kvi.size())) return false;
   if (n_idx > 0 && (!kvi || std::memcmp(kvi, p->fp_kvi.data(), sizeof(int32_t) * n_idx) != 0)) return false;
+  if (p->tree && qo[batch] > 0 &&
+      (!parents || std::memcmp(parents, p->fp_parents.data(), sizeof(int32_t) * qo[batch]) != 0))
+    return false;
   return true;
 }
 
@@ -453,6 +506,8 @@ mla_status attention_launch_of(mla_plan_t p, const void* q_nope, const void* q_p
   ap.rope_dim = p->dims.rope_dim;
   ap.timeout_ns = p->opts.wait_timeout_ns ? p->opts.wait_timeout_ns : 4000000000ull;
   ap.debug_flags = p->opts.debug_flags;
+  ap.tree_items = p->tree ? p->d_tree<TreeItem>(p->sz.off_titems) : nullptr;
+  ap.tree_words = p->tree ? p->d_tree<uint64_t>(p->sz.off_twords) : nullptr;
   a->q_nope = q_nope;
   a->q_pe = q_pe;
   a->cache = cache;
@@ -490,7 +545,7 @@ mla_status enqueue_attention(mla_plan_t p, AttnLaunch& a, cudaStream_t s) {
   if (ev && cudaEventRecord(ev[1], s) != cudaSuccess) return MLA_ERR_CUDA;
   // a graph plan always launches the merge: a later step of the bucket may split
   if (p->sz.cap_merge > 0 && (p->graph || !p->layout.merge.empty())) {
-    MergeParams mp{p->d_merge(), p->d_refs(), a.p.ws_o, a.p.ws_lse, a.p.out, a.p.lse};
+    MergeParams mp{p->d_merge(), p->d_refs(), a.p.ws_o, a.p.ws_lse, a.p.out, a.p.lse, p->tree};
     if (launch_merge(mp, static_cast<int>(p->sz.cap_merge), s) != cudaSuccess) return MLA_ERR_CUDA;
   }
   if (ev) {
@@ -498,6 +553,151 @@ mla_status enqueue_attention(mla_plan_t p, AttnLaunch& a, cudaStream_t s) {
     ++p->runs;
   }
   if (!capturing && cudaEventRecord(p->ev_last, s) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+// Bookkeeping after a launch that reads the plan's device lists.
+mla_status note_launch(mla_plan_t p, cudaStream_t s) {
+  if (stream_capturing(s)) {
+    p->captured = true;
+    return MLA_OK;
+  }
+  return cudaEventRecord(p->ev_last, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+// No C++ exception leaves a C entry: host memory is all that can run out.
+template <typename F>
+mla_status no_throw(F f) noexcept {
+  try {
+    return f();
+  } catch (const std::exception&) {
+    return MLA_ERR_OUT_OF_MEMORY;
+  }
+}
+
+// The layers' caches of one call: present, aligned and apart.
+bool caches_ok(void* const* caches, int32_t n, const mla_dims& d) {
+  const uintptr_t bytes = static_cast<uintptr_t>(d.num_pages) * d.page_size * (kCkv + d.rope_dim) * 2;
+  std::vector<uintptr_t> at(n);
+  for (int32_t i = 0; i < n; ++i) {
+    if (!caches[i] || misaligned16(caches[i])) return false;
+    at[i] = reinterpret_cast<uintptr_t>(caches[i]);
+  }
+  std::sort(at.begin(), at.end());
+  for (int32_t i = 1; i < n; ++i)
+    if (at[i] - at[i - 1] < bytes) return false;
+  return true;
+}
+
+// mla_plan and mla_plan_tree.
+mla_status plan_create(bool tree, const mla_dims* dims, int32_t batch, const int32_t* qo_indptr,
+                       const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* last_page_len,
+                       const int32_t* parents, int32_t causal, void* stream, const mla_plan_options* opts,
+                       mla_plan_t* out_plan) {
+  if (!out_plan) return MLA_ERR_INVALID_ARGUMENT;
+  *out_plan = nullptr;
+  if (!dims || (causal != 0 && causal != 1)) return MLA_ERR_INVALID_ARGUMENT;
+  std::unique_ptr<mla_plan_s, void (*)(mla_plan_s*)> made(new (std::nothrow) mla_plan_s(), free_plan);
+  mla_plan_s* p = made.get();
+  if (!p) return MLA_ERR_OUT_OF_MEMORY;
+  p->dims = *dims;
+  p->tree = tree;
+  p->causal = causal != 0;
+  if (opts) p->opts = *opts;
+  p->host_only = p->opts.host_only != 0;
+  const mla_plan_options& o = p->opts;
+  const int graph_fields = (o.graph_max_batch > 0) + (o.graph_max_tokens > 0) + (o.graph_max_page_ids > 0);
+  if ((graph_fields != 0 && graph_fields != 3) || o.graph_max_batch < 0 || o.graph_max_tokens < 0 ||
+      o.graph_max_page_ids < 0 || (o.context_only != 0 && o.context_only != 1) ||
+      (o.cascade != 0 && o.cascade != 1))
+    return MLA_ERR_INVALID_ARGUMENT;
+  p->graph = graph_fields == 3;
+
+  int num_sms = p->opts.num_sms;
+  if (!p->host_only) {
+    if (cudaGetDevice(&p->device) != cudaSuccess) return MLA_ERR_CUDA;
+    if (num_sms <= 0 &&
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess)
+      return MLA_ERR_CUDA;
+  } else if (num_sms <= 0) {
+    num_sms = 148;
+  }
+  p->opts.num_sms = num_sms;
+
+  if (!fits_bucket(p, batch, qo_indptr, kv_indptr)) return MLA_ERR_INVALID_ARGUMENT;
+  mla_status st = build_layout(request_of(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents), &p->layout);
+  if (st != MLA_OK) return st;
+  remember_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents);
+  if (p->host_only) {
+    *out_plan = made.release();
+    return MLA_OK;
+  }
+
+  // ---- device buffers owned by the plan, uploaded through plan-owned pinned staging
+  const int64_t n_idx = batch > 0 ? kv_indptr[batch] : 0;
+  size_lists(p, p->layout, batch, n_idx);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = reserve_device(p);
+  if (st != MLA_OK) return st;
+  if (p->opts.debug_flags & MLA_DEBUG_KERNEL_TIMING) {
+    p->ring = new (std::nothrow) cudaEvent_t[3 * mla_plan_s::kRing]();
+    if (!p->ring) return MLA_ERR_OUT_OF_MEMORY;
+    for (int i = 0; i < 3 * mla_plan_s::kRing; ++i)
+      if (cudaEventCreate(&p->ring[i]) != cudaSuccess) { cudaGetLastError(); return MLA_ERR_CUDA; }
+  }
+  if (!(p->ev_last = event_take(p->device)) || !(p->h_status = status_slot_take())) return MLA_ERR_CUDA;
+  st = upload(p, kv_indices, n_idx, s);
+  if (st != MLA_OK || cudaEventRecord(p->ev_last, s) != cudaSuccess) {
+    cudaGetLastError();
+    return st != MLA_OK ? st : MLA_ERR_CUDA;
+  }
+  *out_plan = made.release();
+  return MLA_OK;
+}
+
+// mla_plan_update and mla_plan_tree_update.
+mla_status plan_update(bool tree, mla_plan_t p, int32_t batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
+                       const int32_t* kv_indices, const int32_t* last_page_len, const int32_t* parents, void* stream,
+                       int32_t* reused) {
+  if (reused) *reused = 0;
+  if (!p || p->tree != tree) return MLA_ERR_INVALID_ARGUMENT;
+  if (same_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents)) {
+    if (reused) *reused = 1;
+    return MLA_OK;
+  }
+  if (!fits_bucket(p, batch, qo_indptr, kv_indptr)) return MLA_ERR_INVALID_ARGUMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!p->host_only) {
+    if (check_device(p) != MLA_OK || stream_capturing(s)) return MLA_ERR_INVALID_ARGUMENT;
+  }
+  // The new layout is built in the spare one (whose vectors keep their capacity from
+  // earlier steps), then the two are swapped.
+  PlanLayout& L = p->spare;
+  mla_status st = build_layout(request_of(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents), &L);
+  if (st != MLA_OK) return st;
+  reserve_tables(p, batch, qo_indptr, kv_indptr);
+  const int64_t n_idx = batch > 0 ? kv_indptr[batch] : 0;
+  if (p->host_only) {
+    std::swap(p->layout, p->spare);
+    remember_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents);
+    return MLA_OK;
+  }
+  // Size the lists for the new step; a graph plan's sizes are its bucket's and fixed.
+  const mla_plan_s::Sizes saved = p->sz;
+  size_lists(p, L, batch, n_idx);
+  st = reserve_device(p);
+  if (st != MLA_OK) {
+    p->sz = saved;
+    return st;
+  }
+  std::swap(p->layout, p->spare);
+  st = upload(p, kv_indices, n_idx, s);
+  if (st != MLA_OK) {
+    std::swap(p->layout, p->spare);  // the plan keeps describing its previous step
+    return st;
+  }
+  remember_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents);
+  if (cudaEventRecord(p->ev_last, s) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 
@@ -524,112 +724,166 @@ const char* mla_status_string(mla_status s) {
 mla_status mla_plan(const mla_dims* dims, int32_t batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
                     const int32_t* kv_indices, const int32_t* last_page_len, int32_t causal, void* stream,
                     const mla_plan_options* opts, mla_plan_t* out_plan) {
-  if (!out_plan) return MLA_ERR_INVALID_ARGUMENT;
-  *out_plan = nullptr;
-  if (!dims || (causal != 0 && causal != 1)) return MLA_ERR_INVALID_ARGUMENT;
-  mla_plan_s* p = new (std::nothrow) mla_plan_s();
-  if (!p) return MLA_ERR_OUT_OF_MEMORY;
-  p->dims = *dims;
-  p->causal = causal != 0;
-  if (opts) p->opts = *opts;
-  p->host_only = p->opts.host_only != 0;
-  const mla_plan_options& o = p->opts;
-  const int graph_fields = (o.graph_max_batch > 0) + (o.graph_max_tokens > 0) + (o.graph_max_page_ids > 0);
-  if ((graph_fields != 0 && graph_fields != 3) || o.graph_max_batch < 0 || o.graph_max_tokens < 0 ||
-      o.graph_max_page_ids < 0 || (o.context_only != 0 && o.context_only != 1) ||
-      (o.cascade != 0 && o.cascade != 1)) {
-    free_plan(p);
-    return MLA_ERR_INVALID_ARGUMENT;
-  }
-  p->graph = graph_fields == 3;
-
-  int num_sms = p->opts.num_sms;
-  if (!p->host_only) {
-    if (cudaGetDevice(&p->device) != cudaSuccess) { free_plan(p); return MLA_ERR_CUDA; }
-    if (num_sms <= 0) {
-      if (cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess) {
-        free_plan(p);
-        return MLA_ERR_CUDA;
-      }
-    }
-  } else if (num_sms <= 0) {
-    num_sms = 148;
-  }
-  p->opts.num_sms = num_sms;
-
-  if (!fits_bucket(p, batch, qo_indptr, kv_indptr)) { free_plan(p); return MLA_ERR_INVALID_ARGUMENT; }
-  mla_status st = build_layout(request_of(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len), &p->layout);
-  if (st != MLA_OK) { free_plan(p); return st; }
-  remember_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len);
-  if (p->host_only) { *out_plan = p; return MLA_OK; }
-
-  // ---- device buffers owned by the plan, uploaded through plan-owned pinned staging
-  const int64_t n_idx = batch > 0 ? kv_indptr[batch] : 0;
-  size_lists(p, p->layout, n_idx);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = reserve_device(p);
-  if (st != MLA_OK) { free_plan(p); return st; }
-  if (p->opts.debug_flags & MLA_DEBUG_KERNEL_TIMING) {
-    p->ring = new (std::nothrow) cudaEvent_t[3 * mla_plan_s::kRing]();
-    if (!p->ring) { free_plan(p); return MLA_ERR_OUT_OF_MEMORY; }
-    for (int i = 0; i < 3 * mla_plan_s::kRing; ++i)
-      if (cudaEventCreate(&p->ring[i]) != cudaSuccess) { cudaGetLastError(); free_plan(p); return MLA_ERR_CUDA; }
-  }
-  if (!(p->ev_last = event_take(p->device)) || !(p->h_status = status_slot_take())) {
-    free_plan(p);
-    return MLA_ERR_CUDA;
-  }
-  st = upload(p, kv_indices, n_idx, s);
-  if (st != MLA_OK || cudaEventRecord(p->ev_last, s) != cudaSuccess) {
-    cudaGetLastError();
-    free_plan(p);
-    return st != MLA_OK ? st : MLA_ERR_CUDA;
-  }
-  *out_plan = p;
-  return MLA_OK;
+  return no_throw([&] {
+    return plan_create(false, dims, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, nullptr, causal, stream,
+                       opts, out_plan);
+  });
 }
 
 mla_status mla_plan_update(mla_plan_t p, int32_t batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
                            const int32_t* kv_indices, const int32_t* last_page_len, void* stream,
                            int32_t* reused) {
-  if (reused) *reused = 0;
-  if (!p) return MLA_ERR_INVALID_ARGUMENT;
-  if (same_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len)) {
-    if (reused) *reused = 1;
-    return MLA_OK;
-  }
-  if (!fits_bucket(p, batch, qo_indptr, kv_indptr)) return MLA_ERR_INVALID_ARGUMENT;
+  return no_throw([&] {
+    return plan_update(false, p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, nullptr, stream, reused);
+  });
+}
+
+mla_status mla_plan_tree(const mla_dims* dims, int32_t batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
+                         const int32_t* kv_indices, const int32_t* last_page_len, const int32_t* parents,
+                         void* stream, const mla_plan_options* opts, mla_plan_t* out_plan) {
+  return no_throw([&] {
+    return plan_create(true, dims, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents, 1, stream, opts,
+                       out_plan);
+  });
+}
+
+mla_status mla_plan_tree_update(mla_plan_t p, int32_t batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
+                                const int32_t* kv_indices, const int32_t* last_page_len, const int32_t* parents,
+                                void* stream, int32_t* reused) {
+  return no_throw([&] {
+    return plan_update(true, p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents, stream, reused);
+  });
+}
+
+mla_status mla_plan_describe_tree(mla_plan_t p, int32_t* items, int32_t* nodes, uint64_t* words,
+                                  int64_t* num_words) {
+  if (!p || !p->tree) return MLA_ERR_INVALID_ARGUMENT;
+  const PlanLayout& L = p->layout;
+  if (num_words) *num_words = static_cast<int64_t>(L.tree_words.size());
+  if (items && !L.tree_items.empty()) std::memcpy(items, L.tree_items.data(), sizeof(TreeItem) * L.tree_items.size());
+  if (nodes && !L.tree_nodes.empty()) std::memcpy(nodes, L.tree_nodes.data(), sizeof(TreeNode) * L.tree_nodes.size());
+  if (words && !L.tree_words.empty()) std::memcpy(words, L.tree_words.data(), sizeof(uint64_t) * L.tree_words.size());
+  return MLA_OK;
+}
+
+mla_status mla_verify_tree(mla_plan_t p, const int32_t* draft_tokens, const void* target_probs, int64_t ld_target,
+                           const void* draft_probs, int64_t ld_draft, int32_t vocab, mla_prob_type prob_type,
+                           const float* uniform, const float* uniform_next, int32_t* accept_index,
+                           int32_t* num_accepted, int32_t* next_token, void* stream) {
+  if (!p || !p->tree || p->host_only || check_device(p) != MLA_OK) return MLA_ERR_INVALID_ARGUMENT;
+  if (prob_type != MLA_PROB_FP32 && prob_type != MLA_PROB_BF16) return MLA_ERR_INVALID_ARGUMENT;
+  const uintptr_t elem = prob_type == MLA_PROB_FP32 ? 4 : 2;
+  auto off = [](const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) & (a - 1)) != 0; };
+  const int64_t max_ld = int64_t(1) << 40;
+  if (vocab < 1 || vocab > (1 << 28) || ld_target < vocab || ld_target > max_ld || off(target_probs, elem) ||
+      (draft_probs && (ld_draft < vocab || ld_draft > max_ld || off(draft_probs, elem))))
+    return MLA_ERR_INVALID_ARGUMENT;
+  if (p->sz.cap_rows == 0) return MLA_OK;
+  // a step without tokens needs no per-token buffers
+  const bool tokens = p->sz.cap_tokens > 0;
+  if (!num_accepted || !next_token || !uniform_next ||
+      (tokens && (!draft_tokens || !target_probs || !uniform || !accept_index)))
+    return MLA_ERR_INVALID_ARGUMENT;
+  if (off(draft_tokens, 4) || off(uniform, 4) || off(uniform_next, 4) || off(accept_index, 4) || off(num_accepted, 4) ||
+      off(next_token, 4))
+    return MLA_ERR_INVALID_ARGUMENT;
+  if (p->layout.max_nodes > MLA_TREE_MAX_NODES) return MLA_ERR_UNSUPPORTED;
+  VerifyParams v{};
+  v.rows = p->d_tree<TreeRow>(p->sz.off_trows);
+  v.nodes = p->d_tree<TreeNode>(p->sz.off_tnodes);
+  v.draft_tokens = draft_tokens;
+  v.target = target_probs;
+  v.draft = draft_probs;
+  v.ld_target = ld_target;
+  v.ld_draft = ld_draft;
+  v.vocab = vocab;
+  v.uniform = uniform;
+  v.uniform_next = uniform_next;
+  v.accept_index = accept_index;
+  v.num_accepted = num_accepted;
+  v.next_token = next_token;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!p->host_only) {
-    if (check_device(p) != MLA_OK || stream_capturing(s)) return MLA_ERR_INVALID_ARGUMENT;
+  if (launch_verify(v, static_cast<int>(p->sz.cap_rows), prob_type == MLA_PROB_BF16, p->opts.num_sms, s) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return note_launch(p, s);
+}
+
+mla_status mla_compact_kv(mla_plan_t p, const int32_t* accept_index, const int32_t* num_accepted,
+                          void* const* caches, int32_t num_caches, void* stream) {
+  if (!p || !p->tree || p->host_only || check_device(p) != MLA_OK) return MLA_ERR_INVALID_ARGUMENT;
+  if (num_caches < 0 || (num_caches > 0 && !caches) || !p->layout.slots_distinct) return MLA_ERR_INVALID_ARGUMENT;
+  if (num_caches == 0 || p->sz.cap_rows == 0 || p->sz.cap_tokens == 0) return MLA_OK;
+  if (!accept_index || !num_accepted || (reinterpret_cast<uintptr_t>(accept_index) & 3u) ||
+      (reinterpret_cast<uintptr_t>(num_accepted) & 3u))
+    return MLA_ERR_INVALID_ARGUMENT;
+  try {
+    if (!caches_ok(caches, num_caches, p->dims)) return MLA_ERR_INVALID_ARGUMENT;
+  } catch (const std::exception&) {
+    return MLA_ERR_OUT_OF_MEMORY;
   }
-  // The new layout is built in the spare one (whose vectors keep their capacity from
-  // earlier steps), then the two are swapped.
-  PlanLayout& L = p->spare;
-  mla_status st = build_layout(request_of(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len), &L);
-  if (st != MLA_OK) return st;
-  const int64_t n_idx = batch > 0 ? kv_indptr[batch] : 0;
-  if (p->host_only) {
-    std::swap(p->layout, p->spare);
-    remember_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len);
-    return MLA_OK;
+  CompactParams c{};
+  c.rows = p->d_tree<TreeRow>(p->sz.off_trows);
+  c.append_rows = p->d_append();
+  c.accept_index = accept_index;
+  c.num_accepted = num_accepted;
+  c.width = kCkv + p->dims.rope_dim;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (int32_t i = 0; i < num_caches; i += kMaxCaches) {
+    c.num_caches = std::min(kMaxCaches, num_caches - i);
+    for (int32_t k = 0; k < c.num_caches; ++k) c.caches[k] = caches[i + k];
+    if (launch_compact(c, static_cast<int>(p->sz.cap_rows), s) != cudaSuccess) return MLA_ERR_CUDA;
   }
-  // Size the lists for the new step; a graph plan's sizes are its bucket's and fixed.
-  const mla_plan_s::Sizes saved = p->sz;
-  size_lists(p, L, n_idx);
-  st = reserve_device(p);
-  if (st != MLA_OK) {
-    p->sz = saved;
-    return st;
+  return note_launch(p, s);
+}
+
+mla_status mla_copy_pages(const mla_dims* dims, const int32_t* src_pages, const int32_t* dst_pages,
+                          const int32_t* num_tokens, int32_t num_pairs, void* const* caches, int32_t num_caches,
+                          void* stream) {
+  if (!dims || num_pairs < 0 || num_caches < 0 || (num_pairs > 0 && (!src_pages || !dst_pages)) ||
+      (num_caches > 0 && !caches))
+    return MLA_ERR_INVALID_ARGUMENT;
+  const int32_t P = dims->page_size;
+  if (!shape_supported(dims->kv_lora_rank, dims->rope_dim, dims->num_heads, P)) return MLA_ERR_UNSUPPORTED;
+  if (dims->num_pages < 1 || int64_t(dims->num_pages) * P > std::numeric_limits<int32_t>::max() ||
+      !std::isfinite(dims->sm_scale) || !(dims->sm_scale > 0.f))
+    return MLA_ERR_INVALID_ARGUMENT;
+  try {
+    // destinations are distinct and no page is both read and written, so the pairs may run
+    // in any order
+    std::vector<int32_t> to(num_pairs);
+    for (int32_t i = 0; i < num_pairs; ++i) {
+      const int32_t s = src_pages[i], d = dst_pages[i], n = num_tokens ? num_tokens[i] : P;
+      if (s < 0 || s >= dims->num_pages || d < 0 || d >= dims->num_pages || n < 0 || n > P)
+        return MLA_ERR_INVALID_ARGUMENT;
+      to[i] = d;
+    }
+    std::sort(to.begin(), to.end());
+    if (std::adjacent_find(to.begin(), to.end()) != to.end()) return MLA_ERR_INVALID_ARGUMENT;
+    for (int32_t i = 0; i < num_pairs; ++i)
+      if (std::binary_search(to.begin(), to.end(), src_pages[i])) return MLA_ERR_INVALID_ARGUMENT;
+    if (!caches_ok(caches, num_caches, *dims)) return MLA_ERR_INVALID_ARGUMENT;
+  } catch (const std::exception&) {
+    return MLA_ERR_OUT_OF_MEMORY;
   }
-  std::swap(p->layout, p->spare);
-  st = upload(p, kv_indices, n_idx, s);
-  if (st != MLA_OK) {
-    std::swap(p->layout, p->spare);  // the plan keeps describing its previous step
-    return st;
+  const int32_t row_bytes = 2 * (kCkv + dims->rope_dim);
+  CopyParams c{};
+  c.page_bytes = int64_t(P) * row_bytes;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (int32_t i = 0; i < num_pairs; i += kMaxCopyPairs) {
+    c.num_pairs = std::min(kMaxCopyPairs, num_pairs - i);
+    int32_t most = 0;
+    for (int32_t k = 0; k < c.num_pairs; ++k) {
+      const int32_t n = (num_tokens ? num_tokens[i + k] : P) * row_bytes;
+      c.pairs[k] = CopyPair{src_pages[i + k], dst_pages[i + k], n};
+      most = std::max(most, n);
+    }
+    if (most == 0) continue;
+    for (int32_t j = 0; j < num_caches; j += kMaxCaches) {
+      c.num_caches = std::min(kMaxCaches, num_caches - j);
+      for (int32_t k = 0; k < c.num_caches; ++k) c.caches[k] = caches[j + k];
+      if (launch_copy_pages(c, most, s) != cudaSuccess) return MLA_ERR_CUDA;
+    }
   }
-  remember_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len);
-  if (cudaEventRecord(p->ev_last, s) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 

@@ -143,6 +143,8 @@ __device__ __forceinline__ void record_error(int32_t* status, int32_t* mirror, i
 //   exchange : S(j) partial -> peer over DSMEM (st.async, completes the peer's x_full)
 //   softmax  : S(j) = ours + peer's; mask, online softmax, P(j) -> P[j % 2]
 //   PV warp  : PV(j): O += P[j % 2] . V(stage j % 3), as soon as P(j) is written
+// kTree: the step's rows are trees of drafted tokens, masked by the plan's words.
+template <bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
     mla_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                     const __grid_constant__ CUtensorMap tm_kpe, const AttnParams p) {
@@ -389,12 +391,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * q) << 16);
     int vis = w.diag_base + r / p.num_heads + 1;
     vis = max(0, min(vis, w.kv_len));
-    if (r >= w.n_rows) vis = 0;
+    // Rows past the tile's last: their results are not written.  A tree step lets them see
+    // every key, so that they cost no masking (their P rows reach no other row of O).
+    if (r >= w.n_rows) vis = kTree ? w.kv_len : 0;
     const int lim = min(vis, w.key_end);  // keys < lim are visible in this chunk
     const float* xq_ptr = reinterpret_cast<const float*>(smem + kX + q * 8192 + lane * 16);
     const float scale = p.scale_log2;  // > 0 (the planner rejects other scales)
     float m_run = kNegInf, l_run = 0.f;
     bool ok = true;
+    // Tree step: this row's token's mask words, one per key tile from first_tile on (none
+    // for a chain, whose keys are those below lim).
+    const uint64_t* words = nullptr;
+    int first_tile = 0;
+    if (kTree) {
+      const TreeItem ti = p.tree_items[blockIdx.x >> 1];
+      first_tile = ti.first_tile - w.key_begin / kTileN;  // relative to this item's tiles
+      if (ti.words > 0 && r < w.n_rows) words = p.tree_words + ti.word_base + (r / p.num_heads) * ti.words;
+    }
 
     // --- the TMEM part of Q: ckv columns [256r + 192, 256r + 256) and kpe columns
     // [32r, 32r + 32) of this row, as packed bf16 pairs (even element in the low half)
@@ -436,6 +449,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
 
     for (int j = 0; ok && j < ntiles; ++j) {
       const int b2 = j & 1;
+      // read before the wait for S(j), which hides the load
+      uint64_t seen = ~uint64_t(0);
+      if (kTree && words != nullptr && j >= first_tile) seen = __ldg(words + (j - first_tile));
       if (!(ok = wait_warp(bar(bSFull + b2), (j >> 1) & 1, kSiteSoftS, false))) break;
       const int xsl = j % kXSlots, xph = j / kXSlots;
       const uint32_t xfull = bar(bXFull + 4 * xsl + q);
@@ -464,7 +480,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
 
       // --- mask (partial tiles only), running max in the log2 domain, lazy rescale
       const int nvalid = lim - (w.key_begin + kTileN * j);
-      if (__any_sync(0xffffffffu, nvalid < kTileN)) {
+      if (kTree) {
+        if (nvalid < kTileN) seen &= nvalid > 0 ? (uint64_t(1) << nvalid) - 1 : 0;
+        if (__any_sync(0xffffffffu, seen != ~uint64_t(0))) {
+          // A masked node's latent row may hold an infinity or a NaN, and its weight 0 times
+          // that would reach every row of the tile through P.V.  Such a row makes its score
+          // non-finite for every query (0 * t is then NaN), so the scores say when to look;
+          // ckv rows found so in this CTA's half are cleared before P.V(j) is issued.  A
+          // query that does see the key keeps the NaN of its own weight.
+          float odd = 0.f;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) odd = fmaf(t[c], 0.f, odd);
+          if (__any_sync(0xffffffffu, odd != odd)) {
+            const int st = j % kStages;
+            if (!(ok = wait_warp(bar(bKVFull + st), (j / kStages) & 1, kSiteSoftS, false))) break;
+            uint64_t look = 0;  // keys masked here whose score is not finite
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!((seen >> c) & 1) && !(fabsf(t[c]) < -kNegInf)) look |= uint64_t(1) << c;
+            uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(look));
+            uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(look >> 32));
+            uint8_t* v0 = smem + kKV + st * kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
+            for (uint64_t rest = (uint64_t(hi) << 32) | lo; rest != 0; rest &= rest - 1) {
+              uint4* piece = reinterpret_cast<uint4*>(v0 + (__ffsll(static_cast<long long>(rest)) - 1) * 128);
+              const uint4 x = *piece;
+              const uint32_t xs4[4] = {x.x, x.y, x.z, x.w};
+              bool inf_nan = false;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                inf_nan |= (xs4[i] & 0x7f80u) == 0x7f80u || (xs4[i] & 0x7f800000u) == 0x7f800000u;
+              if (inf_nan) *piece = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int c = 0; c < 64; ++c) t[c] = ((seen >> c) & 1) ? t[c] : kNegInf;
+        }
+      } else if (__any_sync(0xffffffffu, nvalid < kTileN)) {
 #pragma unroll
         for (int c = 0; c < 64; ++c) t[c] = (c < nvalid) ? t[c] : kNegInf;
       }
@@ -540,7 +593,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
     // position c ^ R, which keeps both the row-wise writes and the piece-wise reads free
     // of bank conflicts.
     if (ok) {
-      const bool has = l_run > 0.f;
+      // (a tree step's query that sees a NaN key has a NaN sum, which lse reports)
+      const bool has = kTree ? !(l_run <= 0.f) : l_run > 0.f;
       const float inv_l = has ? 1.f / l_run : 0.f;
       const float lse_nat = has ? (m_run + __log2f(l_run)) * 0.69314718055994531f : kNegInf;
       if (ntiles > 0) {
@@ -658,7 +712,9 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MergeParams p) {
         }
         M = Mn;
       }
-      const float wl = (lane < cnt && M != neg_inf) ? __expf(l_l - M) : 0.f;
+      // (a tree step's partial that saw a NaN key carries it on, weight and all)
+      const bool counts = M != neg_inf || (p.tree && l_l != l_l);
+      const float wl = (lane < cnt && counts) ? __expf(l_l - M) : 0.f;
       if (k == 0) {
         float zg = wl;
 #pragma unroll
@@ -677,7 +733,8 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MergeParams p) {
       }
     }
   }
-  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const bool has = z > 0.f || (p.tree && z != z);
+  const float inv = has ? 1.f / z : 0.f;
   uint4 o[2];
   uint32_t* ov = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
@@ -686,7 +743,7 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MergeParams p) {
                                         16 * lane);
   dst[0] = o[0];
   dst[1] = o[1];
-  if (p.lse != nullptr && lane == 0) p.lse[m.q_row0 + r] = z > 0.f ? M + __logf(z) : neg_inf;
+  if (p.lse != nullptr && lane == 0) p.lse[m.q_row0 + r] = has ? M + __logf(z) : neg_inf;
 }
 
 // ---------------------------------------------------------------------- launchers
@@ -732,9 +789,10 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    e = cudaFuncSetAttribute(mla_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(attn::kSmemAlloc));
-    if (e != cudaSuccess) return e;
+    for (auto k : {mla_attn_kernel<false>, mla_attn_kernel<true>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(attn::kSmemAlloc));
+      if (e != cudaSuccess) return e;
+    }
     configured_device = dev;
   }
   AttnParams p = a.p;
@@ -755,8 +813,9 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   } else {
     tm_kpe = tm_kv;
   }
+  const auto kernel = p.tree_items != nullptr ? mla_attn_kernel<true> : mla_attn_kernel<false>;
   if (!a.wait_prior_grid) {
-    mla_attn_kernel<<<2 * a.num_work, attn::kThreads, attn::kSmemAlloc, stream>>>(tm_q, tm_kv, tm_kpe, p);
+    kernel<<<2 * a.num_work, attn::kThreads, attn::kSmemAlloc, stream>>>(tm_q, tm_kv, tm_kpe, p);
     return cudaGetLastError();
   }
   // Programmatic dependent of the append: set-up and query loads overlap it.
@@ -770,7 +829,7 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_attn_kernel, tm_q, tm_kv, tm_kpe, p);
+  return cudaLaunchKernelEx(&cfg, kernel, tm_q, tm_kv, tm_kpe, p);
 }
 
 cudaError_t launch_merge(const MergeParams& p, int num_merge, cudaStream_t stream) {

@@ -44,6 +44,33 @@ struct MergeItem {
 };
 static_assert(sizeof(MergeItem) == 4 * MLA_MERGE_FIELDS, "MergeItem layout");
 
+// A tree plan's mask of one work item: token i of the query tile sees keys below 64 *
+// first_tile and the set bits of words [word_base + i * words, + words), one 64-bit word
+// per key tile from first_tile on.  words == 0: the item's rows are chains, masked by the
+// work item's diag_base alone.
+struct TreeItem {
+  int32_t word_base;
+  int32_t words;
+  int32_t first_tile;
+  int32_t zero;
+};
+static_assert(sizeof(TreeItem) == 4 * MLA_TREE_ITEM_FIELDS, "TreeItem layout");
+
+// A token of a tree step; indices within its row, -1 for none.
+struct TreeNode {
+  int32_t parent;
+  int32_t first_child;
+  int32_t next_sibling;
+  int32_t row;
+};
+static_assert(sizeof(TreeNode) == 4 * MLA_TREE_NODE_FIELDS, "TreeNode layout");
+
+// A row of a tree step; n_nodes == -1 marks an unused row of a graph plan.
+struct TreeRow {
+  int32_t token0;
+  int32_t n_nodes;
+};
+
 // What the planner is asked to plan.
 struct PlanRequest {
   mla_dims d{};
@@ -55,6 +82,8 @@ struct PlanRequest {
   bool causal = true;
   bool context_only = false;
   bool cascade = false;
+  bool tree = false;                 // parents describe each row's nodes (causal)
+  const int32_t* parents = nullptr;  // [T], tree plans only
   int32_t split_keys = 0;
   int32_t num_sms = 148;
   // Upper bounds for a graph plan (0: unbounded).  The planner keeps the split-KV
@@ -72,6 +101,13 @@ struct PlanLayout {
   std::vector<int32_t> refs;         // merge reference list
   std::vector<int32_t> append_rows;  // per token: destination cache row, -1 if none
   bool append_ok = true;             // every token has a slot
+  bool slots_distinct = true;        // no two tokens name one slot
+  // tree plans
+  std::vector<TreeItem> tree_items;  // beside work
+  std::vector<TreeRow> tree_rows;
+  std::vector<TreeNode> tree_nodes;
+  std::vector<uint64_t> tree_words;
+  int32_t max_nodes = 0;             // tokens of the longest row
   int32_t num_partials = 0;
   int32_t ws_rows = 0;               // workspace rows in use
   int32_t num_cascade = 0;           // prefix items of cascaded row groups
@@ -92,6 +128,13 @@ constexpr double kMergeLatency = 1.0;
 
 // Validate the step's tables and build the work and merge lists (host only).
 mla_status build_layout(const PlanRequest& req, PlanLayout* out);
+
+// Mask words of a bucket of `max_tokens` tokens at most: a row of q nodes spans at most
+// (q + 126) / 64 key tiles.
+inline int64_t tree_words_bound(int64_t max_tokens) {
+  const int64_t q = max_tokens < MLA_TREE_MAX_NODES ? max_tokens : MLA_TREE_MAX_NODES;
+  return max_tokens * ((q + 126) / 64);
+}
 
 // Bounds of a graph plan for a bucket of `max_batch` rows and `max_tokens` tokens.
 void graph_bounds(int32_t num_heads, int32_t max_batch, int32_t max_tokens, int32_t num_sms, PlanRequest* req);

@@ -31,6 +31,8 @@ struct AttnParams {
   int32_t rope_dim;  // kpe width: 64, or 0 (cache rows are then 512 wide)
   uint64_t timeout_ns;
   int32_t debug_flags;
+  const TreeItem* tree_items = nullptr;  // tree plans: beside work
+  const uint64_t* tree_words = nullptr;
 };
 
 // Everything one attention launch needs; the launcher encodes the TMA tensor maps from
@@ -54,6 +56,7 @@ struct MergeParams {
   const float* ws_lse;
   void* out;
   float* lse;
+  bool tree;  // of a tree plan
 };
 
 // Latent-cache append: token t's row of src goes to cache row rows[t] (skipped if < 0).
@@ -75,10 +78,60 @@ struct MergeStateParams {
   int64_t rows;
 };
 
+// Verification of drafted trees (mla_verify_tree).
+struct VerifyParams {
+  const TreeRow* rows;
+  const TreeNode* nodes;
+  const int32_t* draft_tokens;
+  const void* target;
+  const void* draft;  // may be null: point masses
+  int64_t ld_target;
+  int64_t ld_draft;
+  int32_t vocab;
+  const float* uniform;
+  const float* uniform_next;
+  int32_t* accept_index;
+  int32_t* num_accepted;
+  int32_t* next_token;
+};
+
+// Layers' caches named by one launch (they travel as kernel parameters).
+constexpr int32_t kMaxCaches = 128;
+
+// Move of the accepted nodes' rows (mla_compact_kv).
+struct CompactParams {
+  const TreeRow* rows;
+  const int32_t* append_rows;  // [tokens]: every step token's cache row
+  const int32_t* accept_index;
+  const int32_t* num_accepted;
+  int32_t width;  // 512 + rope_dim
+  int32_t num_caches;
+  void* caches[kMaxCaches];
+};
+
+// Page copies of one launch (mla_copy_pages).
+struct CopyPair {
+  int32_t src;
+  int32_t dst;
+  int32_t bytes;  // a multiple of the cache row's size
+};
+constexpr int32_t kMaxCopyPairs = 1024;
+struct CopyParams {
+  int64_t page_bytes;
+  int32_t num_pairs;
+  int32_t num_caches;
+  void* caches[kMaxCaches];
+  CopyPair pairs[kMaxCopyPairs];
+};
+
 // cudaErrorInvalidValue when a tensor map cannot be encoded.
 cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, int num_merge, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, int num_tokens, cudaStream_t stream);
 cudaError_t launch_merge_state(const MergeStateParams& p, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyParams& p, int rows, bool bf16, int num_sms, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams& p, int rows, cudaStream_t stream);
+// max_bytes: the largest pair of the launch
+cudaError_t launch_copy_pages(const CopyParams& p, int32_t max_bytes, cudaStream_t stream);
 
 }  // namespace mla

@@ -262,6 +262,88 @@ double estimate(const std::vector<QTile>& tiles, int32_t chunk, int units, int32
   return double(worst) + merge;
 }
 
+// A row whose nodes each continue the one before (a causal row).
+bool is_chain(const int32_t* parents, int32_t n) {
+  for (int32_t i = 0; i < n; ++i)
+    if (parents[i] != i - 1) return false;
+  return true;
+}
+
+// parents[i] in [-1, i) for every node of every row, and no tree beyond the bound.
+bool parents_ok(const int32_t* qo_indptr, int32_t batch, const int32_t* parents) {
+  for (int32_t b = 0; b < batch; ++b) {
+    const int32_t n = qo_indptr[b + 1] - qo_indptr[b];
+    const int32_t* par = parents + qo_indptr[b];
+    for (int32_t i = 0; i < n; ++i)
+      if (par[i] < -1 || par[i] >= i) return false;
+    if (n > MLA_TREE_MAX_NODES && !is_chain(par, n)) return false;
+  }
+  return true;
+}
+
+// A tree step's rows, nodes (children in increasing order) and mask words, and the mask of
+// every work item.  A row's words cover its key tiles from the one that holds its first
+// node, so that one word masks one key tile of one token; the context keys of that first
+// tile are visible to every node.  A node's words are its parent's with its own bit added.
+mla_status build_tree(const PlanRequest& req, PlanLayout* out) {
+  const int32_t batch = req.batch, H = req.d.num_heads;
+  const int32_t T = out->total_tokens;
+  static thread_local std::vector<int32_t> row_words, row_base, last_child;
+  row_words.assign(batch, 0);
+  row_base.assign(batch, 0);
+  out->tree_rows.resize(batch);
+  out->tree_nodes.resize(T);
+  out->tree_words.clear();
+  out->max_nodes = 0;
+  for (int32_t b = 0; b < batch; ++b) {
+    const int32_t t0 = req.qo_indptr[b], n = req.qo_indptr[b + 1] - t0;
+    const int32_t* par = req.parents + t0;
+    out->tree_rows[b] = TreeRow{t0, n};
+    out->max_nodes = std::max(out->max_nodes, n);
+    TreeNode* nodes = out->tree_nodes.data() + t0;
+    last_child.assign(n, -1);
+    for (int32_t i = 0; i < n; ++i) {
+      nodes[i] = TreeNode{par[i], -1, -1, b};
+      if (par[i] < 0) continue;
+      if (last_child[par[i]] < 0)
+        nodes[par[i]].first_child = i;
+      else
+        nodes[last_child[par[i]]].next_sibling = i;
+      last_child[par[i]] = i;
+    }
+    if (n == 0 || is_chain(par, n)) continue;
+    const int32_t k = out->kv_len[b], c = k - n;
+    const int32_t tile0 = c / kTileN, words = (k + kTileN - 1) / kTileN - tile0;
+    const size_t base = out->tree_words.size();
+    if (base + size_t(n) * words > size_t(std::numeric_limits<int32_t>::max())) return MLA_ERR_INVALID_ARGUMENT;
+    row_words[b] = words;
+    row_base[b] = static_cast<int32_t>(base);
+    out->tree_words.resize(base + size_t(n) * words, 0);
+    uint64_t* w = out->tree_words.data() + base;
+    const uint64_t context = (uint64_t(1) << (c - tile0 * kTileN)) - 1;  // keys of tile0 before c
+    for (int32_t i = 0; i < n; ++i) {
+      uint64_t* wi = w + size_t(i) * words;
+      if (par[i] >= 0)
+        std::copy(w + size_t(par[i]) * words, w + size_t(par[i] + 1) * words, wi);
+      else
+        wi[0] = context;
+      const int32_t pos = c + i - tile0 * kTileN;
+      wi[pos / kTileN] |= uint64_t(1) << (pos % kTileN);
+    }
+  }
+  // A cascade item covers several rows but ends with their context (below first_tile), so
+  // its first row's record does for it.
+  out->tree_items.resize(out->work.size());
+  for (size_t i = 0; i < out->work.size(); ++i) {
+    const int32_t t = out->work[i].q_row0 / H;
+    const int32_t b =
+        static_cast<int32_t>(std::upper_bound(req.qo_indptr, req.qo_indptr + batch + 1, t) - req.qo_indptr) - 1;
+    const int32_t t0 = req.qo_indptr[b], c = out->kv_len[b] - (req.qo_indptr[b + 1] - t0);
+    out->tree_items[i] = TreeItem{row_base[b] + (t - t0) * row_words[b], row_words[b], c / kTileN, 0};
+  }
+  return MLA_OK;
+}
+
 }  // namespace
 
 mla_status build_layout(const PlanRequest& req, PlanLayout* out) {
@@ -292,6 +374,9 @@ mla_status build_layout(const PlanRequest& req, PlanLayout* out) {
   }
   const int64_t T = qo_indptr[batch];
   const int64_t n_idx = kv_indptr[batch];
+  if (req.tree && (req.context_only || !req.causal || (T > 0 && !req.parents) ||
+                   !parents_ok(qo_indptr, batch, req.parents)))
+    return MLA_ERR_INVALID_ARGUMENT;
   if (T * H > std::numeric_limits<int32_t>::max() - kTileM) return MLA_ERR_INVALID_ARGUMENT;
   if (n_idx > 0 && !kv_indices) return MLA_ERR_INVALID_ARGUMENT;
   {
@@ -327,8 +412,9 @@ mla_status build_layout(const PlanRequest& req, PlanLayout* out) {
       if (last < 0 || last > P) return MLA_ERR_INVALID_ARGUMENT;
     }
     const int32_t q_b = qo_indptr[b + 1] - qo_indptr[b];
+    if ((req.context_only || req.tree) && k_full[b] < q_b)
+      return MLA_ERR_INVALID_ARGUMENT;  // the tables lack the step's slots
     if (req.context_only) {
-      if (k_full[b] < q_b) return MLA_ERR_INVALID_ARGUMENT;  // the tables lack the step's slots
       out->kv_len[b] = k_full[b] - q_b;
     } else {
       out->kv_len[b] = k_full[b];
@@ -339,6 +425,7 @@ mla_status build_layout(const PlanRequest& req, PlanLayout* out) {
   // --- append slots: token i of row b is key k_b - q_b + i of its row
   out->append_rows.assign(static_cast<size_t>(T), -1);
   out->append_ok = true;
+  out->slots_distinct = true;
   for (int32_t b = 0; b < batch; ++b) {
     const int32_t q_b = qo_indptr[b + 1] - qo_indptr[b];
     for (int32_t i = 0; i < q_b; ++i) {
@@ -368,10 +455,12 @@ mla_status build_layout(const PlanRequest& req, PlanLayout* out) {
       if (row < 0) continue;
       size_t h = (static_cast<uint32_t>(row) * 2654435761u) & mask;
       while (seen[h] >= 0 && seen[h] != row) h = (h + 1) & mask;
-      if (seen[h] == row)
+      if (seen[h] == row) {
         out->append_rows[t] = -1;  // a later token writes this slot
-      else
+        out->slots_distinct = false;
+      } else {
         seen[h] = row;
+      }
     }
   }
 
@@ -434,7 +523,8 @@ mla_status build_layout(const PlanRequest& req, PlanLayout* out) {
           any_query = true;
           const int64_t k_b = out->kv_len[b];
           const bool causal = req.causal && !req.context_only;
-          s = std::min<int64_t>(s, causal ? k_b - q_b + 1 : k_b);
+          // (of a tree, its nodes are not seen by all: the context alone)
+          s = std::min<int64_t>(s, causal ? k_b - q_b + (req.tree ? 0 : 1) : k_b);
         }
         s = s / kTileN * kTileN;
         if (any_query && s >= kTileN) {
@@ -712,7 +802,7 @@ mla_status build_layout(const PlanRequest& req, PlanLayout* out) {
   }
   out->work.resize(sorted.size());
   for (size_t i = 0; i < order.size(); ++i) out->work[i] = sorted[static_cast<uint32_t>(order[i])];
-  return MLA_OK;
+  return req.tree ? build_tree(req, out) : MLA_OK;
 }
 
 }  // namespace mla
