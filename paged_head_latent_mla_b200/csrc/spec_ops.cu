@@ -18,37 +18,40 @@ namespace {
 // the walk need single weights only: p and q at each child's token.  Whole rows of V
 // weights are read where a sum over the vocabulary is needed: after a rejected child that
 // has a next sibling (Z = sum of max(w - Z q, 0)), and once at the end, where the next
-// token is found in the running sum of w.
+// token is found in the running sum of w.  q is read only where a child was rejected.
 //
 // One cluster of C blocks works on a row.  Block 0 gathers the tree's single weights (all
-// nodes at once), walks it, and publishes a command for every pass over a row of weights;
-// the other blocks only follow commands, so that the cluster's barriers match whatever the
-// inputs hold.  In a pass block r sums its C-th of the vocabulary, each warp a contiguous
-// segment of that, and the warps' sums go to block 0's shared memory.  Block 0 finds the
-// segment in which the running sum crosses the target and reads that segment again.
+// nodes at once) into every block's shared memory.  All blocks then walk alike over these
+// copies: what decides a step was written once, to all of them, so that their barriers
+// match whatever the inputs hold.  In a pass block r sums its C-th of the vocabulary, each
+// warp a contiguous segment of that, and every warp's sum goes to all blocks; one cluster
+// barrier per pass (the sums of two passes have buffers of their own: a block can be one
+// barrier ahead of another at most).  The block whose segment the running sum crosses reads
+// that segment again.
 //
 // Weights are held in 64 bits from the first subtraction on: acceptance and the next token
 // are decided at borders, and a sum rounded to 32 bits over a large vocabulary would move
 // a border by more than a token's weight.  Every sum has one fixed order.
-constexpr int kVThreads = 512;
+constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
+constexpr int kVBlocksPerSm = 4;
 constexpr int kVMaxCluster = 8;
 constexpr int kVMaxNodes = MLA_TREE_MAX_NODES;
 
-enum : int32_t { kCmdSum = 0, kCmdExit = 1 };
+// A node as the walk needs it; p, q: the weights of its token at its parent.
+struct WalkNode {
+  int32_t tok;
+  float u, p, q;
+  int32_t first, next;
+};
 
 struct VerifyShared {
-  // block 0: the tree
-  int32_t tok[kVMaxNodes];
-  float u[kVMaxNodes], p[kVMaxNodes], q[kVMaxNodes];  // p, q: weights of tok at the parent
-  int32_t first[kVMaxNodes], next[kVMaxNodes];
-  // every block: the command (written by block 0) and the rejections at its node
-  int32_t cmd, cmd_token, cmd_rejected;
-  double z[kVMaxNodes];        // draft: Z of each rejection
-  int32_t zero[kVMaxNodes];    // point masses: the rejected tokens
-  // block 0: warps' segment sums of the pass
-  double seg[kVMaxCluster * kVWarps];
-  // block 0: search of the crossing
+  WalkNode node[kVMaxNodes];
+  int32_t n;                 // tokens of the row
+  double z[kVMaxNodes];      // draft: Z of each rejection at the walk's node
+  int32_t zero[kVMaxNodes];  // point masses: the tokens rejected there
+  double seg[2][kVMaxCluster * kVWarps];  // warps' sums of a pass
+  // search of the crossing
   double warp_sum[kVWarps];
   int32_t warp_first[kVWarps], warp_last[kVWarps];
 };
@@ -69,27 +72,56 @@ __device__ __forceinline__ float weight(float x) {
   return (x > 0.f && x < __int_as_float(0x7f800000)) ? x : 0.f;
 }
 
-// kVec consecutive weights of a row, chunk c of it: elements [c * kVec - head, + kVec) of
-// which those in [0, V) exist (the others are 0).  `head` makes every whole chunk start on
-// a 16-byte boundary.
+// kVec consecutive weights of a row, kept as loaded until they are used.
 template <typename T, int kVec>
-__device__ __forceinline__ void load_chunk(const T* row, int head, int c, int V, float (&w)[kVec]) {
-  const int e0 = c * kVec - head;
-  if (kVec > 1 && e0 >= 0 && e0 + kVec <= V) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(row + e0));
-    const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      if (sizeof(T) == 4)
-        w[i] = weight(__uint_as_float(r[i & 3]));
-      else
-        w[i] = weight(__uint_as_float((i & 1) ? (r[(i >> 1) & 3] & 0xffff0000u) : (r[(i >> 1) & 3] << 16)));
+struct Chunk {
+  static_assert(kVec == 1 || kVec * sizeof(T) == 16, "one element or 16 bytes");
+  uint32_t r[kVec > 1 ? 4 : 1];
+
+  // Chunk c of the row: elements [c * kVec - head, + kVec) of which those in [0, V) exist
+  // (the others are 0).  `head` makes every whole chunk start on a 16-byte boundary.
+  __device__ __forceinline__ void load(const T* row, int head, int c, int V) {
+    const int e0 = c * kVec - head;
+    if (kVec > 1) {
+      if (e0 >= 0 && e0 + kVec <= V) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + e0));
+        r[0] = x.x;
+        r[1 % (kVec > 1 ? 4 : 1)] = x.y;
+        r[2 % (kVec > 1 ? 4 : 1)] = x.z;
+        r[3 % (kVec > 1 ? 4 : 1)] = x.w;
+        return;
+      }
+      clear();
+      for (int i = 0; i < kVec; ++i)
+        if (e0 + i >= 0 && e0 + i < V) put(i, row[e0 + i]);
+    } else {
+      clear();
+      if (e0 < V) put(0, row[e0]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) w[i] = (e0 + i >= 0 && e0 + i < V) ? weight(to_float(row[e0 + i])) : 0.f;
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (kVec > 1 ? 4 : 1); ++i) r[i] = 0u;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if (sizeof(T) == 4) return weight(__uint_as_float(r[i]));
+    return weight(__uint_as_float((i & 1) ? (r[i >> 1] & 0xffff0000u) : (r[i >> 1] << 16)));
+  }
+
+ private:
+  __device__ __forceinline__ void put(int i, T x) {
+    const float w = to_float(x);
+    const uint32_t bits = __float_as_uint(w);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {  // (registers are not indexed by a variable)
+      if (k != i) continue;
+      if (sizeof(T) == 4)
+        r[k] = bits;
+      else
+        r[k >> 1] |= (k & 1) ? bits : (bits >> 16);
+    }
+  }
+};
 
 // What the rejections at a node leave of a weight.
 __device__ __forceinline__ double left_of(float p, float q, const double* z, int n) {
@@ -106,8 +138,8 @@ template <typename T, int kVec, bool kDraft>
 struct RowPass {
   const T* p;
   const T* q;
-  int head, V, chunks;        // chunks of the row
-  int per_block, per_warp;    // chunks of a block and of a warp's segment
+  int head, V, chunks;      // chunks of the row
+  int per_block, per_warp;  // chunks of a block and of a warp's segment
   const double* z;
   const int32_t* zero;
   int rejected;
@@ -130,11 +162,23 @@ struct RowPass {
     *lo = min(b1, r * per_block + w * per_warp);
     *hi = min(b1, *lo + per_warp);
   }
-  __device__ __forceinline__ void weights(const float (&fp)[kVec], const float (&fq)[kVec], int c,
+  // What is left of chunk c's weights.
+  __device__ __forceinline__ void weights(const Chunk<T, kVec>& cp, const Chunk<T, kVec>& cq, int c,
                                           double (&w)[kVec]) const {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) w[i] = kDraft ? left_of(fp[i], fq[i], z, rejected) : static_cast<double>(fp[i]);
-    if (!kDraft) {
+    for (int i = 0; i < kVec; ++i) w[i] = static_cast<double>(cp.get(i));
+    if (kDraft) {
+      if (rejected > 0) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) w[i] = fmax(w[i] - static_cast<double>(cq.get(i)), 0.0);
+        for (int k = 1; k < rejected; ++k) {
+          const double zk = z[k];
+#pragma unroll
+          for (int i = 0; i < kVec; ++i)
+            w[i] = fmax(__dadd_rn(w[i], -__dmul_rn(zk, static_cast<double>(cq.get(i)))), 0.0);
+        }
+      }
+    } else {
       const int e0 = c * kVec - head;
       for (int k = 0; k < rejected; ++k) {
         const int at = zero[k] - e0;
@@ -145,32 +189,33 @@ struct RowPass {
     }
   }
   // Sum over chunks lo + lane, lo + lane + 32, ...: kBatch chunks' loads in flight.
+  template <int kBatch, bool kQ>
   __device__ __forceinline__ double sum(int lo, int hi, int lane) const {
-    constexpr int kBatch = kVec > 1 ? 4 : 8;
-    double acc[kVec > 1 ? 4 : 1] = {};
+    constexpr int kAcc = kVec > 1 ? 4 : 1;
+    double acc[kAcc] = {};
     for (int c0 = lo + lane; c0 < hi; c0 += 32 * kBatch) {
-      float fp[kBatch][kVec], fq[kBatch][kVec];
+      Chunk<T, kVec> cp[kBatch], cq[kQ ? kBatch : 1];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int c = c0 + 32 * k;
         if (c < hi) {
-          load_chunk<T, kVec>(p, head, c, V, fp[k]);
-          if (kDraft) load_chunk<T, kVec>(q, head, c, V, fq[k]);
+          cp[k].load(p, head, c, V);
+          if (kQ) cq[kQ ? k : 0].load(q, head, c, V);
         } else {
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) fp[k][i] = fq[k][i] = 0.f;
+          cp[k].clear();
+          if (kQ) cq[kQ ? k : 0].clear();
         }
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         double w[kVec];
-        weights(fp[k], fq[k], c0 + 32 * k, w);
+        weights(cp[k], cq[kQ ? k : 0], c0 + 32 * k, w);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[kVec > 1 ? i & 3 : 0] += w[i];
+        for (int i = 0; i < kVec; ++i) acc[i % kAcc] += w[i];
       }
     }
     double t = acc[0];
-    if (kVec > 1) t = (acc[0] + acc[1 % (kVec > 1 ? 4 : 1)]) + (acc[2 % (kVec > 1 ? 4 : 1)] + acc[3 % (kVec > 1 ? 4 : 1)]);
+    if (kAcc == 4) t = (acc[0] + acc[1 % kAcc]) + (acc[2 % kAcc] + acc[3 % kAcc]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
     return t;
@@ -199,125 +244,109 @@ __device__ __forceinline__ double warp_scan(double x, int lane) {
 }
 
 template <typename T, int kVec, bool kDraft>
-__global__ void __launch_bounds__(kVThreads, 2) mla_verify_kernel(const VerifyParams a) {
-  extern __shared__ uint8_t verify_smem[];
+__global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(const VerifyParams a) {
+  extern __shared__ __align__(16) uint8_t verify_smem[];
   VerifyShared& s = *reinterpret_cast<VerifyShared*>(verify_smem);
   uint32_t C;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
   const int rank = static_cast<int>(ptx::cluster_ctarank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / C;
-  const TreeRow row = a.rows[b];
-  const int n = row.n_nodes;
-  if (n < 0) return;  // an unused row of a graph plan: the whole cluster leaves
-  if (n == 0 || n > kVMaxNodes) {
-    if (rank == 0) {
-      if (tid == 0) {
-        a.num_accepted[b] = 0;
-        a.next_token[b] = -1;
+  ptx::cluster_arrive();  // a block's shared memory may be written once it is known to run
+
+  // ---------------------------------------------------------------- gather (block 0)
+  TreeRow row{0, -1};
+  if (rank == 0) {
+    row = a.rows[b];
+    const int n = row.n_nodes, held = n <= kVMaxNodes ? n : 0;
+    const int64_t t0 = row.token0;
+    for (int i = tid; i < n; i += kVThreads) a.accept_index[t0 + i] = (i == 0 && held > 0) ? 0 : -1;
+    for (int i = tid; i < held; i += kVThreads) {
+      const TreeNode nd = a.nodes[t0 + i];
+      WalkNode w{i > 0 ? a.draft_tokens[t0 + i] : -1, a.uniform[t0 + i], 0.f, 0.f, nd.first_child, nd.next_sibling};
+      if (nd.parent >= 0 && w.tok >= 0 && w.tok < a.vocab) {
+        w.p = weight(to_float(static_cast<const T*>(a.target)[(t0 + nd.parent) * a.ld_target + w.tok]));
+        if (kDraft) w.q = weight(to_float(static_cast<const T*>(a.draft)[(t0 + nd.parent) * a.ld_draft + w.tok]));
       }
-      for (int i = tid; i < n; i += kVThreads) a.accept_index[row.token0 + i] = -1;
+      s.node[i] = w;
+    }
+    if (tid == 0) s.n = n;
+    __syncthreads();
+  }
+  ptx::cluster_wait();
+  if (rank == 0 && C > 1) {
+    // copy to the other blocks: the nodes' words, block by block across the warps
+    const int words = s.n > 0 && s.n <= kVMaxNodes ? s.n * static_cast<int>(sizeof(WalkNode) / 4) : 0;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(s.node);
+    const uint32_t at = ptx::smem_addr(s.node), at_n = ptx::smem_addr(&s.n);
+    for (int i = tid; i < words; i += kVThreads) {
+      const uint32_t x = src[i];
+      for (uint32_t r = 1; r < C; ++r) st_cluster_u32(ptx::map_to_cta(at + 4u * i, r), x);
+    }
+    if (tid > 0 && tid < static_cast<int>(C)) st_cluster_u32(ptx::map_to_cta(at_n, tid), static_cast<uint32_t>(s.n));
+    __syncwarp();
+  }
+  cluster_sync();
+
+  const int n = s.n;
+  if (n < 0) return;  // an unused row of a graph plan
+  if (n == 0 || n > kVMaxNodes) {
+    if (rank == 0 && tid == 0) {
+      a.num_accepted[b] = 0;
+      a.next_token[b] = -1;
     }
     return;
   }
-  const int64_t t0 = row.token0;
-  ptx::cluster_arrive();  // a block's shared memory may be written once it is known to run
+  const int64_t t0 = a.rows[b].token0;
+  const int segs = static_cast<int>(C) * kVWarps;
+  const int per = (segs + 31) / 32;  // segments of a lane, in order
+  int flip = 0;                      // the buffer of the last pass's sums
 
-  // One pass over the row of weights of node `node` by the whole cluster (block 0 calls it
-  // with the command published): the warps' sums land in block 0's s.seg.
-  auto pass = [&](int64_t token, int rejected) {
-    const RowPass<T, kVec, kDraft> rp(a, token, rejected, s, C);
+  // One pass over node v's row of weights by the whole cluster; afterwards s.seg[flip]
+  // holds every warp's sum in every block, and the return value is their total.
+  auto run_pass = [&](int v, int rejected) -> double {
+    __syncthreads();  // the list of rejections is written
+    flip ^= 1;
+    const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, s, C);
     int lo, hi;
     rp.segment(rank, warp, &lo, &hi);
-    const double t = rp.sum(lo, hi, lane);
-    if (lane == 0) st_cluster_f64(ptx::map_to_cta(ptx::smem_addr(&s.seg[rank * kVWarps + warp]), 0), t);
+    double t;
+    if (kDraft && rejected > 0)
+      t = rp.template sum<(kVec > 1 ? 2 : 8), true>(lo, hi, lane);
+    else
+      t = rp.template sum<(kVec > 1 ? 4 : 8), false>(lo, hi, lane);
+    if (lane < static_cast<int>(C))
+      st_cluster_f64(ptx::map_to_cta(ptx::smem_addr(&s.seg[flip][rank * kVWarps + warp]), lane), t);
     __syncwarp();
     cluster_sync();
-  };
-
-  if (rank != 0) {
-    ptx::cluster_wait();
-    while (true) {
-      cluster_sync();  // the command is there
-      if (s.cmd == kCmdExit) return;
-      pass(t0 + s.cmd_token, s.cmd_rejected);
-    }
-  }
-
-  // ---------------------------------------------------------------- block 0
-  for (int i = tid; i < n; i += kVThreads) {
-    const TreeNode nd = a.nodes[t0 + i];
-    const int x = i > 0 ? a.draft_tokens[t0 + i] : -1;
-    s.tok[i] = x;
-    s.u[i] = a.uniform[t0 + i];
-    s.first[i] = nd.first_child;
-    s.next[i] = nd.next_sibling;
-    float p = 0.f, q = 0.f;
-    if (nd.parent >= 0 && x >= 0 && x < a.vocab) {
-      p = weight(to_float(static_cast<const T*>(a.target)[(t0 + nd.parent) * a.ld_target + x]));
-      if (kDraft) q = weight(to_float(static_cast<const T*>(a.draft)[(t0 + nd.parent) * a.ld_draft + x]));
-    }
-    s.p[i] = p;
-    s.q[i] = q;
-    a.accept_index[t0 + i] = i == 0 ? 0 : -1;
-  }
-  __syncthreads();
-  ptx::cluster_wait();
-
-  // Publish a pass and run it; afterwards every thread may read s.seg.  The rejections
-  // (s.z or s.zero) are copied to the other blocks with the command.
-  auto run_pass = [&](int node, int rejected) {
-    __syncthreads();
-    for (uint32_t r = 1 + warp; r < C; r += kVWarps) {
-      for (int k = lane; k < rejected; k += 32) {
-        if (kDraft)
-          st_cluster_f64(ptx::map_to_cta(ptx::smem_addr(&s.z[k]), r), s.z[k]);
-        else
-          st_cluster_u32(ptx::map_to_cta(ptx::smem_addr(&s.zero[k]), r), static_cast<uint32_t>(s.zero[k]));
-      }
-      if (lane == 0) {
-        st_cluster_u32(ptx::map_to_cta(ptx::smem_addr(&s.cmd), r), kCmdSum);
-        st_cluster_u32(ptx::map_to_cta(ptx::smem_addr(&s.cmd_token), r), static_cast<uint32_t>(node));
-        st_cluster_u32(ptx::map_to_cta(ptx::smem_addr(&s.cmd_rejected), r), static_cast<uint32_t>(rejected));
-      }
-    }
-    __syncwarp();
-    cluster_sync();
-    pass(t0 + node, rejected);
-  };
-  const int segs = static_cast<int>(C) * kVWarps;
-  // Inclusive running sum at segment i of this lane's share (lane l owns segments [l * per,
-  // (l + 1) * per)); the same in every warp.
-  const int per = (segs + 31) / 32;
-  auto total = [&]() -> double {
-    double t = 0.0;
+    double mine = 0.0;
     for (int i = 0; i < per; ++i)
-      if (lane * per + i < segs) t += s.seg[lane * per + i];
-    return __shfl_sync(0xffffffffu, warp_scan(t, lane), 31);
+      if (lane * per + i < segs) mine += s.seg[flip][lane * per + i];
+    return __shfl_sync(0xffffffffu, warp_scan(mine, lane), 31);
   };
 
+  // ---------------------------------------------------------------- walk (all blocks alike)
   int v = 0, kept = 1, rejected = 0;
   while (true) {
-    // every thread walks alike over the same shared values
-    int c = s.first[v], got = -1;
+    int c = s.node[v].first, got = -1;
     double Z = 1.0;
     rejected = 0;
-    for (; c >= 0; c = s.next[c]) {
-      const int x = s.tok[c];
-      if (x < 0) {  // given
+    for (; c >= 0; c = s.node[c].next) {
+      const WalkNode nd = s.node[c];
+      if (nd.tok < 0) {  // given
         got = c;
         break;
       }
       double w;
       if (kDraft) {
-        w = left_of(s.p[c], s.q[c], s.z, rejected);
+        w = left_of(nd.p, nd.q, s.z, rejected);
       } else {
-        w = s.p[c];
+        w = nd.p;
         for (int k = 0; k < rejected; ++k)
-          if (s.zero[k] == x) w = 0.0;
+          if (s.zero[k] == nd.tok) w = 0.0;
       }
-      const double u = s.u[c];
-      const double limit = kDraft ? __dmul_rn(__dmul_rn(u, static_cast<double>(s.q[c])), Z) : __dmul_rn(u, Z);
+      const double u = nd.u;
+      const double limit = kDraft ? __dmul_rn(__dmul_rn(u, static_cast<double>(nd.q)), Z) : __dmul_rn(u, Z);
       if (limit < w) {
         got = c;
         break;
@@ -326,14 +355,9 @@ __global__ void __launch_bounds__(kVThreads, 2) mla_verify_kernel(const VerifyPa
       if (kDraft) {
         if (tid == 0) s.z[rejected] = Z;
         ++rejected;
-        if (s.next[c] >= 0) {
-          run_pass(v, rejected);
-          Z = total();
-        } else {
-          __syncthreads();
-        }
+        if (nd.next >= 0) Z = run_pass(v, rejected);
       } else {
-        if (tid == 0) s.zero[rejected] = x;
+        if (tid == 0) s.zero[rejected] = nd.tok;
         ++rejected;
         Z = fmax(Z - w, 0.0);
         __syncthreads();
@@ -341,118 +365,111 @@ __global__ void __launch_bounds__(kVThreads, 2) mla_verify_kernel(const VerifyPa
     }
     if (got < 0) break;
     v = got;
-    if (tid == 0) a.accept_index[t0 + kept] = v;
+    if (rank == 0 && tid == 0) a.accept_index[t0 + kept] = v;
     ++kept;
   }
 
-  run_pass(v, rejected);
-  double W = total();
+  double W = run_pass(v, rejected);
   if (!(W > 0.0) && rejected > 0) {
     rejected = 0;
-    run_pass(v, 0);
-    W = total();
+    W = run_pass(v, 0);
   }
-  // dismiss the other blocks
-  for (uint32_t r = 1 + warp; r < C; r += kVWarps)
-    if (lane == 0) st_cluster_u32(ptx::map_to_cta(ptx::smem_addr(&s.cmd), r), kCmdExit);
-  __syncwarp();
-  ptx::cluster_arrive();
+  if (rank == 0 && tid == 0) a.num_accepted[b] = kept;
+  if (!(W > 0.0)) {
+    if (rank == 0 && tid == 0) a.next_token[b] = -1;
+    return;
+  }
 
-  int token = -1;
-  if (W > 0.0) {
-    const double target = __dmul_rn(static_cast<double>(a.uniform_next[b]), W);
-    // the first segment whose inclusive running sum exceeds the target, else the last one
-    // that holds any weight
-    double mine = 0.0;
-    for (int i = 0; i < per; ++i)
-      if (lane * per + i < segs) mine += s.seg[lane * per + i];
-    double run = warp_scan(mine, lane);
-    run = __shfl_up_sync(0xffffffffu, run, 1);
-    if (lane == 0) run = 0.0;
-    int hit = segs, last = -1;
-    double before_hit = 0.0, before_last = 0.0;
-    for (int i = 0; i < per; ++i) {
-      const int g = lane * per + i;
-      if (g >= segs) break;
-      const double t = s.seg[g];
-      if (t > 0.0) {
-        if (hit == segs && run + t > target) {
-          hit = g;
-          before_hit = run;
-        }
-        last = g;
-        before_last = run;
+  // ---------------------------------------------------------------- the next token
+  // The first segment whose inclusive running sum exceeds the target, else the last one
+  // that holds any weight; the same in every warp.
+  const double target = __dmul_rn(static_cast<double>(a.uniform_next[b]), W);
+  const double* seg = s.seg[flip];
+  double mine = 0.0;
+  for (int i = 0; i < per; ++i)
+    if (lane * per + i < segs) mine += seg[lane * per + i];
+  double run = warp_scan(mine, lane);
+  run = __shfl_up_sync(0xffffffffu, run, 1);
+  if (lane == 0) run = 0.0;
+  int hit = segs, last = -1;
+  double before_hit = 0.0, before_last = 0.0;
+  for (int i = 0; i < per; ++i) {
+    const int g = lane * per + i;
+    if (g >= segs) break;
+    const double t = seg[g];
+    if (t > 0.0) {
+      if (hit == segs && run + t > target) {
+        hit = g;
+        before_hit = run;
       }
-      run += t;
+      last = g;
+      before_last = run;
     }
-    const int best = __reduce_min_sync(0xffffffffu, hit);
-    const int tail = __reduce_max_sync(0xffffffffu, last);
-    const int g = best < segs ? best : tail;
-    double base = best < segs ? before_hit : before_last;
-    const unsigned owner = __ballot_sync(0xffffffffu, (best < segs ? hit : last) == g);
-    base = __shfl_sync(0xffffffffu, base, __ffs(owner) - 1);
+    run += t;
+  }
+  const int best = __reduce_min_sync(0xffffffffu, hit);
+  const int tail = __reduce_max_sync(0xffffffffu, last);
+  const int g = best < segs ? best : tail;
+  if (g / kVWarps != rank) return;
+  double base = best < segs ? before_hit : before_last;
+  const unsigned owner = __ballot_sync(0xffffffffu, (best < segs ? hit : last) == g);
+  base = __shfl_sync(0xffffffffu, base, __ffs(owner) - 1);
 
-    // read the segment again, the whole block at once, in order
-    const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, s, C);
-    int lo, hi;
-    rp.segment(g / kVWarps, g % kVWarps, &lo, &hi);
-    int last_seen = -1;
-    for (int c0 = lo; c0 < hi && token < 0; c0 += kVThreads) {
-      const int c = c0 + tid;
-      float fp[kVec], fq[kVec];
-      double w[kVec];
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) fp[i] = fq[i] = 0.f;
-      if (c < hi) {
-        load_chunk<T, kVec>(rp.p, rp.head, c, rp.V, fp);
-        if (kDraft) load_chunk<T, kVec>(rp.q, rp.head, c, rp.V, fq);
-      }
-      rp.weights(fp, fq, c, w);
-      double sum = 0.0;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) sum += w[i];
-      const double incl = warp_scan(sum, lane);
-      if (lane == 31) s.warp_sum[warp] = incl;
-      __syncthreads();
-      double run2 = base;
-      for (int k = 0; k < warp; ++k) run2 += s.warp_sum[k];
-      double all = base;
-      for (int k = 0; k < kVWarps; ++k) all += s.warp_sum[k];
-      const double prev = __shfl_up_sync(0xffffffffu, incl, 1);
-      run2 += lane > 0 ? prev : 0.0;
-      int first = 0x7fffffff, fin = -1;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        run2 += w[i];
-        if (w[i] > 0.0) {
-          const int e = c * kVec - rp.head + i;
-          if (first == 0x7fffffff && run2 > target) first = e;
-          fin = e;
-        }
-      }
-      first = __reduce_min_sync(0xffffffffu, first);
-      fin = __reduce_max_sync(0xffffffffu, fin);
-      if (lane == 0) {
-        s.warp_first[warp] = first;
-        s.warp_last[warp] = fin;
-      }
-      __syncthreads();
-      for (int k = kVWarps - 1; k >= 0; --k) {
-        if (s.warp_first[k] != 0x7fffffff) token = s.warp_first[k];
-        last_seen = max(last_seen, s.warp_last[k]);
-      }
-      base = all;
-      __syncthreads();
+  // read the segment again, the whole block at once, in order
+  const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, s, C);
+  int lo, hi;
+  rp.segment(rank, g % kVWarps, &lo, &hi);
+  int token = -1, last_seen = -1;
+  for (int c0 = lo; c0 < hi && token < 0; c0 += kVThreads) {
+    const int c = c0 + tid;
+    Chunk<T, kVec> cp, cq;
+    cp.clear();
+    cq.clear();
+    if (c < hi) {
+      cp.load(rp.p, rp.head, c, rp.V);
+      if (kDraft && rejected > 0) cq.load(rp.q, rp.head, c, rp.V);
     }
-    // rounding may leave the crossing just past the segment's last weight
-    if (token < 0) token = last_seen;
+    double w[kVec];
+    rp.weights(cp, cq, c, w);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) sum += w[i];
+    const double incl = warp_scan(sum, lane);
+    if (lane == 31) s.warp_sum[warp] = incl;
+    __syncthreads();
+    double run2 = base, all = base;
+    for (int k = 0; k < kVWarps; ++k) {
+      if (k < warp) run2 += s.warp_sum[k];
+      all += s.warp_sum[k];
+    }
+    const double prev = __shfl_up_sync(0xffffffffu, incl, 1);
+    run2 += lane > 0 ? prev : 0.0;
+    int first = 0x7fffffff, fin = -1;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      run2 += w[i];
+      if (w[i] > 0.0) {
+        const int e = c * kVec - rp.head + i;
+        if (first == 0x7fffffff && run2 > target) first = e;
+        fin = e;
+      }
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    fin = __reduce_max_sync(0xffffffffu, fin);
+    if (lane == 0) {
+      s.warp_first[warp] = first;
+      s.warp_last[warp] = fin;
+    }
+    __syncthreads();
+    for (int k = kVWarps - 1; k >= 0; --k) {
+      if (s.warp_first[k] != 0x7fffffff) token = s.warp_first[k];
+      last_seen = max(last_seen, s.warp_last[k]);
+    }
+    base = all;
+    __syncthreads();
   }
-  if (tid == 0) {
-    a.num_accepted[b] = kept;
-    a.next_token[b] = token;
-  }
-  __syncwarp();
-  ptx::cluster_wait();
+  // rounding may leave the crossing just past the segment's last weight
+  if (tid == 0) a.next_token[b] = token < 0 ? last_seen : token;
 }
 
 // ------------------------------------------------------------------ compaction
@@ -541,9 +558,9 @@ static_assert(sizeof(VerifyShared) <= 48 * 1024, "fits without an opt-in");
 }  // namespace
 
 cudaError_t launch_verify(const VerifyParams& p, int rows, bool bf16, int num_sms, cudaStream_t stream) {
-  // As many blocks to a row as keep every cluster resident at once (two blocks to an SM).
+  // As many blocks to a row as keep every cluster resident at once.
   int cluster = kVMaxCluster;
-  while (cluster > 1 && static_cast<int64_t>(rows) * cluster > 2 * static_cast<int64_t>(num_sms)) cluster /= 2;
+  while (cluster > 1 && static_cast<int64_t>(rows) * cluster > int64_t(kVBlocksPerSm) * num_sms) cluster /= 2;
   // Whole 16-byte loads where p's and q's rows have the same offset from a 16-byte boundary.
   const int64_t es = bf16 ? 2 : 4;
   const bool vec = !p.draft || (((p.ld_target - p.ld_draft) * es) % 16 == 0 &&
