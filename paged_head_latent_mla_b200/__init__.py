@@ -178,6 +178,27 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+_helpers = None
+# element types of the native argument checks
+_BF16, _F32, _I32 = 0, 1, 2
+
+
+def _native():
+    """The binding's native argument checks (built with the library)."""
+    global _helpers
+    if _helpers is None:
+        import importlib
+
+        import torch  # noqa: F401  (its libraries must be loaded first)
+
+        try:
+            _helpers = importlib.import_module("._marshal", __name__)
+        except ImportError as e:
+            raise RuntimeError("the binding's native part is missing or stale: python -m "
+                               "paged_head_latent_mla_b200._build --force") from e
+    return _helpers
+
+
 def status_string(status: int) -> str:
     return load_library().mla_status_string(int(status)).decode()
 
@@ -202,7 +223,7 @@ def _i32(x) -> np.ndarray:
 
 def _ptr(a: np.ndarray) -> int:
     """Address of a host int32 array's data, for the table arguments (declared void*)."""
-    return a.ctypes.data
+    return a.ctypes.data if _helpers is None else _helpers.address(a)
 
 
 def mla_supports(kv_lora_rank: int, rope_dim: int, num_heads: int, page_size: int) -> bool:
@@ -213,7 +234,8 @@ class MlaPlan:
     """Owns one C plan handle (``mla_plan_t``); destroyed with the object."""
 
     def __init__(self, handle: int, batch: int, num_heads: int, total_tokens: int, graph_max_tokens: int = 0,
-                 rope_dim: int = ROPE_DIM, num_pages: int = 0, page_size: int = 0, graph_max_batch: int = 0):
+                 rope_dim: int = ROPE_DIM, num_pages: int = 0, page_size: int = 0, graph_max_batch: int = 0,
+                 tree: bool = False):
         self._h = ctypes.c_void_p(handle)
         self.batch = batch
         self.num_heads = num_heads
@@ -225,6 +247,7 @@ class MlaPlan:
         # a graph plan's per-token buffers hold graph_max_tokens tokens
         self.graph_max_tokens = graph_max_tokens
         self.graph_max_batch = graph_max_batch
+        self.tree = tree
 
     @property
     def batch_capacity(self) -> int:
@@ -285,7 +308,8 @@ def _make_plan(who, tables, extra, dims, opts, stream) -> MlaPlan:
         raise MlaError(st, who)
     graph = opts.graph_max_tokens > 0
     return MlaPlan(out.value, batch, dims.num_heads, int(qo[-1]), opts.graph_max_tokens if graph else 0,
-                   dims.rope_dim, dims.num_pages, dims.page_size, opts.graph_max_batch if graph else 0)
+                   dims.rope_dim, dims.num_pages, dims.page_size, opts.graph_max_batch if graph else 0,
+                   who == "mla_plan_tree")
 
 
 def mla_plan(qo_indptr, kv_indptr, kv_indices, last_page_len, *, num_heads: int, page_size: int, num_pages: int,
@@ -390,57 +414,46 @@ def mla_run(plan: MlaPlan, q_nope, q_pe, cache, out=None, lse=None, return_lse: 
     With ``kv_new`` ([T, 512 + rope_dim] bf16) the step's latent rows are first written
     into the cache (``mla_run_append``).  ``q_pe`` may be None for a plan with
     ``rope_dim=0``."""
-    import torch
-
+    N = _native()
     T, H, R = plan.token_capacity, plan.num_heads, plan.rope_dim
-    width = KV_LORA_RANK + R
-    _check_cache_shape(cache, plan.num_pages, plan.page_size, R)
-    _check_dev_tensor(q_nope, "q_nope", torch.bfloat16, (T, H, KV_LORA_RANK))
-    if R > 0 or q_pe is not None:
-        _check_dev_tensor(q_pe, "q_pe", torch.bfloat16, (T, H, R))
-    _check_dev_tensor(cache, "cache", torch.bfloat16, tuple(cache.shape))
+    # a tree plan's tensors must be on the current device (which is the plan's)
+    dev = N.device() if plan.tree else -1
+    cache_p = N.cache(cache, dev, plan.num_pages, plan.page_size, KV_LORA_RANK + R)
+    rows = (T, H, KV_LORA_RANK)
+    q_p = N.tensor(q_nope, "q_nope", _BF16, dev, rows)
+    qpe_p = N.tensor(q_pe, "q_pe", _BF16, dev, (T, H, R)) if R > 0 or q_pe is not None else 0
+    on = q_nope.get_device()
     if out is None:
-        out = torch.empty((T, H, KV_LORA_RANK), dtype=torch.bfloat16, device=q_nope.device)
-    _check_dev_tensor(out, "out", torch.bfloat16, (T, H, KV_LORA_RANK))
+        out = N.empty(_BF16, on, rows)
+    out_p = N.tensor(out, "out", _BF16, dev, rows)
     if return_lse and lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q_nope.device)
-    if lse is not None:
-        _check_dev_tensor(lse, "lse", torch.float32, (T, H))
-    if kv_new is not None:
-        _check_dev_tensor(kv_new, "kv_new", torch.bfloat16, (T, width))
+        lse = N.empty(_F32, on, (T, H))
+    lse_p = N.tensor(lse, "lse", _F32, dev, (T, H)) if lse is not None else 0
     if stream is None:
-        stream = torch.cuda.current_stream(q_nope.device).cuda_stream
-    lib = load_library()
-    lse_p = ctypes.c_void_p(lse.data_ptr() if lse is not None else 0)
-    qpe_p = ctypes.c_void_p(q_pe.data_ptr() if q_pe is not None else 0)
+        stream = N.stream(on)
     if kv_new is None:
-        st = lib.mla_run(plan.handle, ctypes.c_void_p(q_nope.data_ptr()), qpe_p,
-                         ctypes.c_void_p(cache.data_ptr()), ctypes.c_void_p(out.data_ptr()), lse_p,
-                         ctypes.c_void_p(stream or 0))
+        st = load_library().mla_run(plan.handle, q_p, qpe_p, cache_p, out_p, lse_p, stream)
         what = "mla_run"
     else:
-        st = lib.mla_run_append(plan.handle, ctypes.c_void_p(q_nope.data_ptr()), qpe_p,
-                                ctypes.c_void_p(kv_new.data_ptr()), ctypes.c_void_p(cache.data_ptr()),
-                                ctypes.c_void_p(out.data_ptr()), lse_p, ctypes.c_void_p(stream or 0))
+        new_p = N.tensor(kv_new, "kv_new", _BF16, dev, (T, KV_LORA_RANK + R))
+        st = load_library().mla_run_append(plan.handle, q_p, qpe_p, new_p, cache_p, out_p, lse_p, stream)
         what = "mla_run_append"
     if st != MLA_OK:
         raise MlaError(st, what)
-    return (out, lse) if (return_lse or lse is not None) else out
+    return (out, lse) if lse is not None else out
 
 
 def mla_append_kv(plan: MlaPlan, kv_new, cache, stream=None) -> None:
     """Write the step's latent rows ``kv_new`` [T, 576] into their cache slots
     (``mla_append_kv``)."""
-    import torch
-
+    N = _native()
     width = KV_LORA_RANK + plan.rope_dim
-    _check_cache_shape(cache, plan.num_pages, plan.page_size, plan.rope_dim)
-    _check_dev_tensor(kv_new, "kv_new", torch.bfloat16, (plan.token_capacity, width))
-    _check_dev_tensor(cache, "cache", torch.bfloat16, tuple(cache.shape))
+    dev = N.device() if plan.tree else -1
+    cache_p = N.cache(cache, dev, plan.num_pages, plan.page_size, width)
+    new_p = N.tensor(kv_new, "kv_new", _BF16, dev, (plan.token_capacity, width))
     if stream is None:
-        stream = torch.cuda.current_stream(kv_new.device).cuda_stream
-    st = load_library().mla_append_kv(plan.handle, ctypes.c_void_p(kv_new.data_ptr()),
-                                      ctypes.c_void_p(cache.data_ptr()), ctypes.c_void_p(stream or 0))
+        stream = N.stream(kv_new.get_device())
+    st = load_library().mla_append_kv(plan.handle, new_p, cache_p, stream)
     if st != MLA_OK:
         raise MlaError(st, "mla_append_kv")
 
@@ -598,28 +611,6 @@ def mla_plan_describe_tree(plan: MlaPlan) -> dict:
     return {"items": items[: info["num_work"]], "nodes": nodes[: info["total_tokens"]], "words": words[: n.value]}
 
 
-def _check_current_device(*tensors) -> None:
-    import torch
-
-    for t in tensors:
-        if t is not None and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors must be on the current device, got {t.device}")
-
-
-def _check_rows(t, name, dtype, tokens: int, vocab: int):
-    """A [tokens, vocab] CUDA tensor whose rows are contiguous (any row pitch)."""
-    import torch
-
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (tokens, vocab):
-        raise ValueError(f"{name} must have shape {(tokens, vocab)}, got {tuple(t.shape)}")
-    if vocab > 1 and t.stride(1) != 1 or tokens > 1 and t.stride(0) < vocab:
-        raise ValueError(f"{name} must have contiguous rows")
-
-
 def mla_verify_tree(plan: MlaPlan, draft_tokens, target_probs, uniform, uniform_next, draft_probs=None,
                     accept_index=None, num_accepted=None, next_token=None, stream=None):
     """Verify a tree plan's drafted tokens against the target's probabilities, from given
@@ -627,80 +618,48 @@ def mla_verify_tree(plan: MlaPlan, draft_tokens, target_probs, uniform, uniform_
     point masses) are [T, vocab] fp32 or bf16 with contiguous rows; ``draft_tokens`` [T]
     int32; ``uniform`` [T] and ``uniform_next`` [batch] fp32.  Returns (accept_index [T],
     num_accepted [batch], next_token [batch]), int32."""
-    import torch
-
-    T, B = plan.token_capacity, plan.batch_capacity
-    if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2 or target_probs.shape[1] < 1:
-        raise ValueError("target_probs must be a [T, vocab] tensor")
-    if target_probs.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"target_probs must be float32 or bfloat16, got {target_probs.dtype}")
-    V, kind, dev = target_probs.shape[1], target_probs.dtype, target_probs.device
-    _check_rows(target_probs, "target_probs", kind, T, V)
-    if draft_probs is not None:
-        _check_rows(draft_probs, "draft_probs", kind, T, V)
-    _check_dev_tensor(draft_tokens, "draft_tokens", torch.int32, (T,))
-    _check_dev_tensor(uniform, "uniform", torch.float32, (T,))
-    _check_dev_tensor(uniform_next, "uniform_next", torch.float32, (B,))
+    N = _native()
+    T, B, dev = plan.token_capacity, plan.batch_capacity, N.device()
+    kind = str(getattr(target_probs, "dtype", None))
+    if kind not in ("torch.float32", "torch.bfloat16") or target_probs.dim() != 2 or target_probs.shape[1] < 1:
+        raise ValueError("target_probs must be a [T, vocab] tensor of float32 or bfloat16")
+    code, V = (_F32, _BF16)[kind == "torch.bfloat16"], target_probs.shape[1]
+    target_p, target_ld = N.rows(target_probs, "target_probs", code, dev, T, V)
+    draft_p, draft_ld = N.rows(draft_probs, "draft_probs", code, dev, T, V) if draft_probs is not None else (0, 0)
+    tok_p = N.tensor(draft_tokens, "draft_tokens", _I32, dev, (T,))
+    u_p = N.tensor(uniform, "uniform", _F32, dev, (T,))
+    un_p = N.tensor(uniform_next, "uniform_next", _F32, dev, (B,))
     if accept_index is None:
-        accept_index = torch.empty(T, dtype=torch.int32, device=dev)
+        accept_index = N.empty(_I32, dev, (T,))
     if num_accepted is None:
-        num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        num_accepted = N.empty(_I32, dev, (B,))
     if next_token is None:
-        next_token = torch.empty(B, dtype=torch.int32, device=dev)
-    _check_dev_tensor(accept_index, "accept_index", torch.int32, (T,))
-    _check_dev_tensor(num_accepted, "num_accepted", torch.int32, (B,))
-    _check_dev_tensor(next_token, "next_token", torch.int32, (B,))
-    _check_current_device(target_probs, draft_probs, draft_tokens, uniform, uniform_next, accept_index, num_accepted,
-                          next_token)
+        next_token = N.empty(_I32, dev, (B,))
+    acc_p = N.tensor(accept_index, "accept_index", _I32, dev, (T,))
+    cnt_p = N.tensor(num_accepted, "num_accepted", _I32, dev, (B,))
+    nxt_p = N.tensor(next_token, "next_token", _I32, dev, (B,))
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-
-    def pitch(t):
-        return max(V, t.stride(0)) if T > 1 else V
-
-    vp = ctypes.c_void_p
-    st = load_library().mla_verify_tree(
-        plan.handle, vp(draft_tokens.data_ptr()), vp(target_probs.data_ptr()), pitch(target_probs),
-        vp(draft_probs.data_ptr() if draft_probs is not None else 0),
-        pitch(draft_probs) if draft_probs is not None else 0, V,
-        MLA_PROB_FP32 if kind == torch.float32 else MLA_PROB_BF16, vp(uniform.data_ptr()),
-        vp(uniform_next.data_ptr()), vp(accept_index.data_ptr()), vp(num_accepted.data_ptr()),
-        vp(next_token.data_ptr()), vp(stream or 0))
+        stream = N.stream(dev)
+    st = load_library().mla_verify_tree(plan.handle, tok_p, target_p, target_ld, draft_p, draft_ld, V,
+                                        MLA_PROB_FP32 if code == _F32 else MLA_PROB_BF16, u_p, un_p, acc_p, cnt_p,
+                                        nxt_p, stream)
     if st != MLA_OK:
         raise MlaError(st, "mla_verify_tree")
     return accept_index, num_accepted, next_token
-
-
-def _cache_list(caches):
-    """The layers' caches of one call: a list of tensors [num_pages, page_size, width], or
-    one tensor with a leading layer dimension (or none, for a single layer)."""
-    import torch
-
-    if isinstance(caches, torch.Tensor):
-        caches = list(caches.unbind(0)) if caches.dim() == 4 else [caches]
-    return list(caches)
 
 
 def mla_compact_kv(plan: MlaPlan, accept_index, num_accepted, caches, stream=None) -> None:
     """Move the accepted nodes' latent rows to consecutive cache slots in every layer's
     cache, in place (``mla_compact_kv``).  ``caches``: a list of [num_pages, page_size,
     512 + rope_dim] tensors, or one tensor with a leading layer dimension."""
-    import torch
-
-    caches = _cache_list(caches)
-    width = KV_LORA_RANK + plan.rope_dim
-    for c in caches:
-        _check_cache_shape(c, plan.num_pages, plan.page_size, plan.rope_dim)
-        _check_dev_tensor(c, "cache", torch.bfloat16, (c.shape[0], plan.page_size, width))
-    _check_dev_tensor(accept_index, "accept_index", torch.int32, (plan.token_capacity,))
-    _check_dev_tensor(num_accepted, "num_accepted", torch.int32, (plan.batch_capacity,))
-    _check_current_device(accept_index, num_accepted, *caches)
+    N = _native()
+    dev = N.device()
+    ptrs = N.caches(caches, dev, plan.num_pages, plan.page_size, KV_LORA_RANK + plan.rope_dim)
+    acc_p = N.tensor(accept_index, "accept_index", _I32, dev, (plan.token_capacity,))
+    cnt_p = N.tensor(num_accepted, "num_accepted", _I32, dev, (plan.batch_capacity,))
     if stream is None:
-        stream = torch.cuda.current_stream(accept_index.device).cuda_stream
-    ptrs = (ctypes.c_void_p * max(1, len(caches)))(*[c.data_ptr() for c in caches])
-    st = load_library().mla_compact_kv(plan.handle, ctypes.c_void_p(accept_index.data_ptr()),
-                                       ctypes.c_void_p(num_accepted.data_ptr()), ptrs, len(caches),
-                                       ctypes.c_void_p(stream or 0))
+        stream = N.stream(dev)
+    st = load_library().mla_compact_kv(plan.handle, acc_p, cnt_p, ptrs, len(ptrs) // 8, stream)
     if st != MLA_OK:
         raise MlaError(st, "mla_compact_kv")
 
@@ -708,30 +667,26 @@ def mla_compact_kv(plan: MlaPlan, accept_index, num_accepted, caches, stream=Non
 def mla_copy_pages(src_pages, dst_pages, caches, num_tokens=None, stream=None) -> None:
     """Copy the first ``num_tokens[i]`` tokens (None: all) of page ``src_pages[i]`` to page
     ``dst_pages[i]`` in every layer's cache (``mla_copy_pages``).  The tables are host
-    arrays; ``caches`` as for ``mla_compact_kv``, all of one shape and on the current
-    device."""
-    import torch
-
-    caches = _cache_list(caches)
+    arrays; ``caches`` as for ``mla_compact_kv``, on the current device and with as many
+    pages as the first at least."""
     src, dst = _i32(src_pages), _i32(dst_pages)
     tok = None if num_tokens is None else _i32(num_tokens)
     if src.ndim != 1 or dst.shape != src.shape or (tok is not None and tok.shape != src.shape):
         raise MlaError(MLA_ERR_INVALID_ARGUMENT, "mla_copy_pages: table lengths")
-    if not caches:
+    if len(caches) == 0:
         return
-    shape = tuple(getattr(caches[0], "shape", ()))
+    shape = caches.shape[-3:] if hasattr(caches, "shape") else getattr(caches[0], "shape", ())
     if len(shape) != 3:
         raise ValueError("caches must be [num_pages, page_size, 512 + rope_dim]")
-    for c in caches:
-        _check_dev_tensor(c, "cache", torch.bfloat16, shape)
-    _check_current_device(*caches)
+    N = _native()
+    dev = N.device()
+    ptrs = N.caches(caches, dev, *shape)
     if stream is None:
-        stream = torch.cuda.current_stream(caches[0].device).cuda_stream
+        stream = N.stream(dev)
     dims = _Dims(128, KV_LORA_RANK, shape[2] - KV_LORA_RANK, shape[1], shape[0], 1.0)
-    ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
-    st = load_library().mla_copy_pages(ctypes.byref(dims), _ptr(src), _ptr(dst),
-                                       None if tok is None else _ptr(tok), len(src), ptrs, len(caches),
-                                       ctypes.c_void_p(stream or 0))
+    st = load_library().mla_copy_pages(ctypes.byref(dims), N.address(src), N.address(dst),
+                                       None if tok is None else N.address(tok), len(src), ptrs, len(ptrs) // 8,
+                                       stream)
     if st != MLA_OK:
         raise MlaError(st, "mla_copy_pages")
 

@@ -14,6 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmla_b200.so")
 SOURCES = ["api.cu", "mla_attn.cu", "state_ops.cu", "spec_ops.cu", "plan.cpp", "noalloc.cu"]
+MARSHAL = os.path.join(PKG, "_marshal.so")  # the Python binding's argument checks
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 HEADERS = ["mla_internal.h", "mla_launch.h", "sm100_ptx.cuh"]
 
 
@@ -24,15 +26,43 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def needs_build() -> bool:
-    if not os.path.exists(LIB):
+def _older(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "mla.h")]
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def needs_build() -> bool:
+    return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "mla.h")])
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile the binding's native part against the installed torch (host code only)."""
+    if not force and not _older(MARSHAL, [MARSHAL_SOURCE]):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi())]
+    for d in inc:
+        cmd += ["-isystem", d]
+    cmd += [MARSHAL_SOURCE, "-o", MARSHAL + ".tmp"]
+    cmd += ["-L" + os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_marshal(force)
     if not force and not needs_build():
         return LIB
     cmd = [
