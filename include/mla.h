@@ -378,7 +378,8 @@ typedef enum { MLA_PROB_FP32 = 0, MLA_PROB_BF16 = 1 } mla_prob_type;
  *     else, before the next child:  w = max(w - Z q, 0),  Z = sum of w
  * and an accepted child is the next v.  Where every child was rejected (or v has none),
  * w as the rejections left it (p where that is zero everywhere) gives the next token: the
- * first x whose running sum of w exceeds uniform_next[b] * (sum of w).
+ * first x whose running sum of w exceeds uniform_next[b] * (sum of w), or the last x of
+ * positive weight where rounding leaves none.
  * Without draft_probs the drafted tokens are point masses: a child is accepted if
  * uniform[c] * Z < w(x), else w(x) = 0 and Z = max(Z - w(x), 0).
  * A draft token < 0 was given, not drafted: it is accepted without a test.  One >= vocab

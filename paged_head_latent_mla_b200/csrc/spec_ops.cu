@@ -29,7 +29,7 @@ namespace {
 // barrier ahead of another at most).  The block whose segment the running sum crosses reads
 // that segment again.
 //
-// Weights are held in 64 bits from the first subtraction on: acceptance and the next token
+// Weights are held in 64 bits from the first subtraction on (one rounding): acceptance and the next token
 // are decided at borders, and a sum rounded to 32 bits over a large vocabulary would move
 // a border by more than a token's weight.  Every sum has one fixed order.
 constexpr int kVThreads = 256;
@@ -47,9 +47,9 @@ struct WalkNode {
 
 struct VerifyShared {
   WalkNode node[kVMaxNodes];
-  int32_t n;                 // tokens of the row
-  double z[kVMaxNodes];      // draft: Z of each rejection at the walk's node
-  int32_t zero[kVMaxNodes];  // point masses: the tokens rejected there
+  int32_t n;       // tokens of the row
+  int32_t token0;  // its first
+  int32_t zero[kVMaxNodes];  // point masses: the tokens rejected at the walk's node
   double seg[2][kVMaxCluster * kVWarps];  // warps' sums of a pass
   // search of the crossing
   double warp_sum[kVWarps];
@@ -103,9 +103,28 @@ struct Chunk {
 #pragma unroll
     for (int i = 0; i < (kVec > 1 ? 4 : 1); ++i) r[i] = 0u;
   }
+  // Element i as it is stored.
   __device__ __forceinline__ float get(int i) const {
-    if (sizeof(T) == 4) return weight(__uint_as_float(r[i]));
-    return weight(__uint_as_float((i & 1) ? (r[i >> 1] & 0xffff0000u) : (r[i >> 1] << 16)));
+    if (sizeof(T) == 4) return __uint_as_float(r[i]);
+    return __uint_as_float((i & 1) ? (r[i >> 1] & 0xffff0000u) : (r[i >> 1] << 16));
+  }
+  // All elements' bits: no sign and no top exponent bit among them means that every one is
+  // in [0, 2), which probabilities are, and a weight as it stands.
+  __device__ __forceinline__ uint32_t bits() const {
+    return kVec > 1 ? (r[0] | r[1 % (kVec > 1 ? 4 : 1)]) | (r[2 % (kVec > 1 ? 4 : 1)] | r[3 % (kVec > 1 ? 4 : 1)])
+                    : r[0];
+  }
+  static constexpr uint32_t kOddBits = sizeof(T) == 4 ? 0xc0000000u : 0xc000c000u;
+  // Replace elements that count as 0.
+  __device__ __forceinline__ void clean() {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      if (weight(get(i)) != 0.f) continue;
+      if (sizeof(T) == 4)
+        r[i] = 0u;
+      else
+        r[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+    }
   }
 
  private:
@@ -123,15 +142,13 @@ struct Chunk {
   }
 };
 
-// What the rejections at a node leave of a weight.
-__device__ __forceinline__ double left_of(float p, float q, const double* z, int n) {
-  double w = static_cast<double>(p);
-  if (n > 0) {
-    const double dq = static_cast<double>(q);
-    w = fmax(w - dq, 0.0);  // the first Z is 1
-    for (int k = 1; k < n; ++k) w = fmax(__dadd_rn(w, -__dmul_rn(z[k], dq)), 0.0);
-  }
-  return w;
+// What rejections at a node leave of a weight.  Taking Z q off and cutting at 0, once per
+// rejection, is taking off the sum S of all Z at once: max(max(w - a, 0) - b, 0) is
+// max(w - a - b, 0) for a, b >= 0.  So a pass costs the same after any number of
+// rejections.
+__device__ __forceinline__ double left_of(double p, double q, double S) {
+  const double d = __fma_rn(-S, q, p);
+  return d > 0.0 ? d : 0.0;
 }
 
 template <typename T, int kVec, bool kDraft>
@@ -140,19 +157,20 @@ struct RowPass {
   const T* q;
   int head, V, chunks;      // chunks of the row
   int per_block, per_warp;  // chunks of a block and of a warp's segment
-  const double* z;
-  const int32_t* zero;
+  double S;             // draft: sum of the rejections' Z, 0 without one
+  const int32_t* zero;  // point masses: the rejected tokens
   int rejected;
 
-  __device__ RowPass(const VerifyParams& a, int64_t token, int nrej, const VerifyShared& s, int cluster) {
+  __device__ RowPass(const VerifyParams& a, int64_t token, int nrej, double sum_z, const VerifyShared& s,
+                     int cluster) {
     p = static_cast<const T*>(a.target) + token * a.ld_target;
     q = kDraft ? static_cast<const T*>(a.draft) + token * a.ld_draft : nullptr;
     V = a.vocab;
     head = kVec > 1 ? static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T)) : 0;
     chunks = static_cast<int>((static_cast<int64_t>(V) + head + kVec - 1) / kVec);
-    per_block = (chunks + cluster - 1) / cluster;
+    per_block = (chunks + cluster - 1) >> (__ffs(cluster) - 1);  // clusters are powers of two
     per_warp = (per_block + kVWarps - 1) / kVWarps;
-    z = s.z;
+    S = sum_z;
     zero = s.zero;
     rejected = nrej;
   }
@@ -162,29 +180,24 @@ struct RowPass {
     *lo = min(b1, r * per_block + w * per_warp);
     *hi = min(b1, *lo + per_warp);
   }
-  // What is left of chunk c's weights.
+  // What is left of (clean) chunk c's weights; kQ: a child was rejected.
+  template <bool kQ>
   __device__ __forceinline__ void weights(const Chunk<T, kVec>& cp, const Chunk<T, kVec>& cq, int c,
                                           double (&w)[kVec]) const {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) w[i] = static_cast<double>(cp.get(i));
-    if (kDraft) {
-      if (rejected > 0) {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) w[i] = fmax(w[i] - static_cast<double>(cq.get(i)), 0.0);
-        for (int k = 1; k < rejected; ++k) {
-          const double zk = z[k];
-#pragma unroll
-          for (int i = 0; i < kVec; ++i)
-            w[i] = fmax(__dadd_rn(w[i], -__dmul_rn(zk, static_cast<double>(cq.get(i)))), 0.0);
-        }
-      }
-    } else {
+    for (int i = 0; i < kVec; ++i) {
+      w[i] = static_cast<double>(cp.get(i));
+      if (kQ) w[i] = left_of(w[i], static_cast<double>(cq.get(i)), S);
+    }
+    if (!kDraft) {
       const int e0 = c * kVec - head;
       for (int k = 0; k < rejected; ++k) {
         const int at = zero[k] - e0;
+        if (static_cast<unsigned>(at) < static_cast<unsigned>(kVec)) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          if (at == i) w[i] = 0.0;
+          for (int i = 0; i < kVec; ++i)
+            if (at == i) w[i] = 0.0;
+        }
       }
     }
   }
@@ -208,8 +221,13 @@ struct RowPass {
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
+        Chunk<T, kVec>& q0 = cq[kQ ? k : 0];
+        if ((cp[k].bits() | (kQ ? q0.bits() : 0u)) & Chunk<T, kVec>::kOddBits) {
+          cp[k].clean();
+          if (kQ) q0.clean();
+        }
         double w[kVec];
-        weights(cp[k], cq[kQ ? k : 0], c0 + 32 * k, w);
+        weights<kQ>(cp[k], q0, c0 + 32 * k, w);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) acc[i % kAcc] += w[i];
       }
@@ -270,7 +288,10 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
       }
       s.node[i] = w;
     }
-    if (tid == 0) s.n = n;
+    if (tid == 0) {
+      s.n = n;
+      s.token0 = row.token0;
+    }
     __syncthreads();
   }
   ptx::cluster_wait();
@@ -278,12 +299,16 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
     // copy to the other blocks: the nodes' words, block by block across the warps
     const int words = s.n > 0 && s.n <= kVMaxNodes ? s.n * static_cast<int>(sizeof(WalkNode) / 4) : 0;
     const uint32_t* src = reinterpret_cast<const uint32_t*>(s.node);
-    const uint32_t at = ptx::smem_addr(s.node), at_n = ptx::smem_addr(&s.n);
+    const uint32_t at = ptx::smem_addr(s.node), at_n = ptx::smem_addr(&s.n),
+                   at_t = ptx::smem_addr(&s.token0);
     for (int i = tid; i < words; i += kVThreads) {
       const uint32_t x = src[i];
       for (uint32_t r = 1; r < C; ++r) st_cluster_u32(ptx::map_to_cta(at + 4u * i, r), x);
     }
-    if (tid > 0 && tid < static_cast<int>(C)) st_cluster_u32(ptx::map_to_cta(at_n, tid), static_cast<uint32_t>(s.n));
+    if (tid > 0 && tid < static_cast<int>(C)) {
+      st_cluster_u32(ptx::map_to_cta(at_n, tid), static_cast<uint32_t>(s.n));
+      st_cluster_u32(ptx::map_to_cta(at_t, tid), static_cast<uint32_t>(s.token0));
+    }
     __syncwarp();
   }
   cluster_sync();
@@ -297,22 +322,24 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
     }
     return;
   }
-  const int64_t t0 = a.rows[b].token0;
+  const int64_t t0 = s.token0;
+  // (read now, needed at the end)
+  const double u_next = static_cast<double>(a.uniform_next[b]);
   const int segs = static_cast<int>(C) * kVWarps;
   const int per = (segs + 31) / 32;  // segments of a lane, in order
   int flip = 0;                      // the buffer of the last pass's sums
 
   // One pass over node v's row of weights by the whole cluster; afterwards s.seg[flip]
   // holds every warp's sum in every block, and the return value is their total.
-  auto run_pass = [&](int v, int rejected) -> double {
-    __syncthreads();  // the list of rejections is written
+  auto run_pass = [&](int v, int rejected, double S) -> double {
+    if (!kDraft) __syncthreads();  // the list of rejections is written
     flip ^= 1;
-    const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, s, C);
+    const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, S, s, C);
     int lo, hi;
     rp.segment(rank, warp, &lo, &hi);
     double t;
     if (kDraft && rejected > 0)
-      t = rp.template sum<(kVec > 1 ? 2 : 8), true>(lo, hi, lane);
+      t = rp.template sum<(kVec > 4 ? 2 : 4), kDraft>(lo, hi, lane);
     else
       t = rp.template sum<(kVec > 1 ? 4 : 8), false>(lo, hi, lane);
     if (lane < static_cast<int>(C))
@@ -327,21 +354,22 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
 
   // ---------------------------------------------------------------- walk (all blocks alike)
   int v = 0, kept = 1, rejected = 0;
+  double S = 0.0;  // draft: the sum of the rejections' Z
   while (true) {
     int c = s.node[v].first, got = -1;
     double Z = 1.0;
     rejected = 0;
+    S = 0.0;
     for (; c >= 0; c = s.node[c].next) {
       const WalkNode nd = s.node[c];
       if (nd.tok < 0) {  // given
         got = c;
         break;
       }
-      double w;
+      double w = nd.p;
       if (kDraft) {
-        w = left_of(nd.p, nd.q, s.z, rejected);
+        w = left_of(w, nd.q, S);
       } else {
-        w = nd.p;
         for (int k = 0; k < rejected; ++k)
           if (s.zero[k] == nd.tok) w = 0.0;
       }
@@ -351,14 +379,13 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
         got = c;
         break;
       }
-      __syncthreads();  // all have read the list
+      ++rejected;
       if (kDraft) {
-        if (tid == 0) s.z[rejected] = Z;
-        ++rejected;
-        if (nd.next >= 0) Z = run_pass(v, rejected);
+        S += Z;
+        if (nd.next >= 0) Z = run_pass(v, rejected, S);
       } else {
-        if (tid == 0) s.zero[rejected] = nd.tok;
-        ++rejected;
+        __syncthreads();  // all have read the list
+        if (tid == 0) s.zero[rejected - 1] = nd.tok;
         Z = fmax(Z - w, 0.0);
         __syncthreads();
       }
@@ -369,10 +396,10 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
     ++kept;
   }
 
-  double W = run_pass(v, rejected);
+  double W = run_pass(v, rejected, S);
   if (!(W > 0.0) && rejected > 0) {
     rejected = 0;
-    W = run_pass(v, 0);
+    W = run_pass(v, 0, 0.0);
   }
   if (rank == 0 && tid == 0) a.num_accepted[b] = kept;
   if (!(W > 0.0)) {
@@ -383,7 +410,7 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
   // ---------------------------------------------------------------- the next token
   // The first segment whose inclusive running sum exceeds the target, else the last one
   // that holds any weight; the same in every warp.
-  const double target = __dmul_rn(static_cast<double>(a.uniform_next[b]), W);
+  const double target = __dmul_rn(u_next, W);
   const double* seg = s.seg[flip];
   double mine = 0.0;
   for (int i = 0; i < per; ++i)
@@ -416,7 +443,7 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
   base = __shfl_sync(0xffffffffu, base, __ffs(owner) - 1);
 
   // read the segment again, the whole block at once, in order
-  const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, s, C);
+  const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, S, s, C);
   int lo, hi;
   rp.segment(rank, g % kVWarps, &lo, &hi);
   int token = -1, last_seen = -1;
@@ -429,8 +456,13 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
       cp.load(rp.p, rp.head, c, rp.V);
       if (kDraft && rejected > 0) cq.load(rp.q, rp.head, c, rp.V);
     }
+    cp.clean();
+    cq.clean();
     double w[kVec];
-    rp.weights(cp, cq, c, w);
+    if (kDraft && rejected > 0)
+      rp.template weights<kDraft>(cp, cq, c, w);
+    else
+      rp.template weights<false>(cp, cq, c, w);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) sum += w[i];
