@@ -137,6 +137,25 @@ __device__ __forceinline__ void record_error(int32_t* status, int32_t* mirror, i
 
 }  // namespace attn
 
+// Set the elements of a stage's ckv rows that are not finite to 0 (one warp).  A query that
+// sees such a key keeps the NaN of its own weight; the others must not meet 0 * NaN.
+__device__ __noinline__ void clear_non_finite(uint8_t* stage, int lane) {
+  for (int i = lane; i < static_cast<int>(attn::kStageKpe / 16); i += 32) {
+    uint4* piece = reinterpret_cast<uint4*>(stage + 16 * i);
+    uint4 x = *piece;
+    uint32_t v[4] = {x.x, x.y, x.z, x.w};
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if ((v[k] & 0x7f80u) == 0x7f80u) v[k] &= 0xffff0000u, odd = true;
+      if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0x0000ffffu, odd = true;
+    }
+    if (odd) *piece = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // Pipeline per 64-key tile j (phases of every two-buffer barrier are j >> 1):
 //   producer : KV(j) -> stage j % 3                        (after PV(j - 3) freed it)
 //   QK warp  : QK(j) -> S[j % 2], as soon as KV(j) landed and S(j - 2) was read
@@ -167,9 +186,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return sb + kBar + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kMisc + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMisc);
+  // [j % 4]: j if tile j has a score that is not finite (tree steps).  A slot is written again
+  // four tiles on, after the wait for PV(j + 1).
+  volatile int* odd_tile = reinterpret_cast<volatile int*>(smem + kMisc + 16);
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    for (int i = 0; kTree && i < 4; ++i) odd_tile[i] = -1;
     mbar_init(bar(bQFull), 1);
     mbar_init(bar(bQTmem), 4);
     for (int s = 0; s < kStages; ++s) {
@@ -337,6 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
       for (int j = 0; j < ntiles; ++j) {
         if (!wait_warp(bar(bPFull + (j & 1)), (j >> 1) & 1, kSiteMmaP, false)) break;
         tc_fence_after();
+        if (kTree && odd_tile[j & 3] == j) clear_non_finite(smem + kKV + (j % kStages) * kStageBytes, lane);
         if (lane == 0) {
           const uint32_t kv = sb + kKV + (j % kStages) * kStageBytes;
           const uint32_t pcol = tmem + kColP + 32 * (j & 1);
@@ -399,14 +423,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
     const float scale = p.scale_log2;  // > 0 (the planner rejects other scales)
     float m_run = kNegInf, l_run = 0.f;
     bool ok = true;
-    // Tree step: this row's token's mask words, one per key tile from first_tile on (none
-    // for a chain, whose keys are those below lim).
-    const uint64_t* words = nullptr;
-    int first_tile = 0;
-    if (kTree) {
+    // Tree step: this row's token has a mask word for each key tile from tile mask_from on
+    // (none for a chain, whose keys are those below lim): word word0 + j for tile j.
+    int mask_from = 0x7fffffff, word0 = 0;
+    if (kTree && r < w.n_rows) {
       const TreeItem ti = p.tree_items[blockIdx.x >> 1];
-      first_tile = ti.first_tile - w.key_begin / kTileN;  // relative to this item's tiles
-      if (ti.words > 0 && r < w.n_rows) words = p.tree_words + ti.word_base + (r / p.num_heads) * ti.words;
+      if (ti.words > 0) {
+        mask_from = ti.first_tile - w.key_begin / kTileN;  // relative to this item's tiles
+        word0 = ti.word_base + (r / p.num_heads) * ti.words - mask_from;
+      }
     }
 
     // --- the TMEM part of Q: ckv columns [256r + 192, 256r + 256) and kpe columns
@@ -449,9 +474,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
 
     for (int j = 0; ok && j < ntiles; ++j) {
       const int b2 = j & 1;
-      // read before the wait for S(j), which hides the load
-      uint64_t seen = ~uint64_t(0);
-      if (kTree && words != nullptr && j >= first_tile) seen = __ldg(words + (j - first_tile));
+      // (fetched during the wait for S(j); a register held from here on would spill)
+      if (kTree && j >= mask_from) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.tree_words + (word0 + j)));
       if (!(ok = wait_warp(bar(bSFull + b2), (j >> 1) & 1, kSiteSoftS, false))) break;
       const int xsl = j % kXSlots, xph = j / kXSlots;
       const uint32_t xfull = bar(bXFull + 4 * xsl + q);
@@ -481,39 +505,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
       // --- mask (partial tiles only), running max in the log2 domain, lazy rescale
       const int nvalid = lim - (w.key_begin + kTileN * j);
       if (kTree) {
-        if (nvalid < kTileN) seen &= nvalid > 0 ? (uint64_t(1) << nvalid) - 1 : 0;
-        if (__any_sync(0xffffffffu, seen != ~uint64_t(0))) {
+        if (__any_sync(0xffffffffu, nvalid < kTileN || j >= mask_from)) {
+          uint64_t seen = j >= mask_from ? __ldg(p.tree_words + (word0 + j)) : ~uint64_t(0);
+          if (nvalid < kTileN) seen &= nvalid > 0 ? (uint64_t(1) << nvalid) - 1 : 0;
           // A masked node's latent row may hold an infinity or a NaN, and its weight 0 times
           // that would reach every row of the tile through P.V.  Such a row makes its score
-          // non-finite for every query (0 * t is then NaN), so the scores say when to look;
-          // ckv rows found so in this CTA's half are cleared before P.V(j) is issued.  A
-          // query that does see the key keeps the NaN of its own weight.
+          // non-finite for every query (0 * t is then NaN): the PV warp is told to look.
           float odd = 0.f;
 #pragma unroll
           for (int c = 0; c < 64; ++c) odd = fmaf(t[c], 0.f, odd);
-          if (__any_sync(0xffffffffu, odd != odd)) {
-            const int st = j % kStages;
-            if (!(ok = wait_warp(bar(bKVFull + st), (j / kStages) & 1, kSiteSoftS, false))) break;
-            uint64_t look = 0;  // keys masked here whose score is not finite
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!((seen >> c) & 1) && !(fabsf(t[c]) < -kNegInf)) look |= uint64_t(1) << c;
-            uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(look));
-            uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(look >> 32));
-            uint8_t* v0 = smem + kKV + st * kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
-            for (uint64_t rest = (uint64_t(hi) << 32) | lo; rest != 0; rest &= rest - 1) {
-              uint4* piece = reinterpret_cast<uint4*>(v0 + (__ffsll(static_cast<long long>(rest)) - 1) * 128);
-              const uint4 x = *piece;
-              const uint32_t xs4[4] = {x.x, x.y, x.z, x.w};
-              bool inf_nan = false;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                inf_nan |= (xs4[i] & 0x7f80u) == 0x7f80u || (xs4[i] & 0x7f800000u) == 0x7f800000u;
-              if (inf_nan) *piece = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+          if (odd != odd) odd_tile[j & 3] = j;
 #pragma unroll
           for (int c = 0; c < 64; ++c) t[c] = ((seen >> c) & 1) ? t[c] : kNegInf;
         }
