@@ -589,6 +589,31 @@ bool caches_ok(void* const* caches, int32_t n, const mla_dims& d) {
   return true;
 }
 
+// Enqueue checked page copies, as many launches as the parameters' lists ask for.
+template <typename Params>
+mla_status copy_pages(const mla_dims& d, const int32_t* src, const int32_t* dst, const int32_t* num_tokens,
+                      int32_t num_pairs, void* const* caches, int32_t num_caches, cudaStream_t s) {
+  const int32_t row_bytes = 2 * (kCkv + d.rope_dim);
+  Params c;
+  c.page_bytes = int64_t(d.page_size) * row_bytes;
+  for (int32_t i = 0; i < num_pairs; i += Params::max_pairs) {
+    c.num_pairs = std::min(Params::max_pairs, num_pairs - i);
+    int32_t most = 0;
+    for (int32_t k = 0; k < c.num_pairs; ++k) {
+      const int32_t n = (num_tokens ? num_tokens[i + k] : d.page_size) * row_bytes;
+      c.pairs[k] = CopyPair{src[i + k], dst[i + k], n};
+      most = std::max(most, n);
+    }
+    if (most == 0) continue;
+    for (int32_t j = 0; j < num_caches; j += Params::max_caches) {
+      c.num_caches = std::min(Params::max_caches, num_caches - j);
+      for (int32_t k = 0; k < c.num_caches; ++k) c.caches[k] = caches[j + k];
+      if (launch_copy_pages(c, most, s) != cudaSuccess) return MLA_ERR_CUDA;
+    }
+  }
+  return MLA_OK;
+}
+
 // mla_plan and mla_plan_tree.
 mla_status plan_create(bool tree, const mla_dims* dims, int32_t batch, const int32_t* qo_indptr,
                        const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* last_page_len,
@@ -865,26 +890,10 @@ mla_status mla_copy_pages(const mla_dims* dims, const int32_t* src_pages, const 
   } catch (const std::exception&) {
     return MLA_ERR_OUT_OF_MEMORY;
   }
-  const int32_t row_bytes = 2 * (kCkv + dims->rope_dim);
-  CopyParams c{};
-  c.page_bytes = int64_t(P) * row_bytes;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  for (int32_t i = 0; i < num_pairs; i += kMaxCopyPairs) {
-    c.num_pairs = std::min(kMaxCopyPairs, num_pairs - i);
-    int32_t most = 0;
-    for (int32_t k = 0; k < c.num_pairs; ++k) {
-      const int32_t n = (num_tokens ? num_tokens[i + k] : P) * row_bytes;
-      c.pairs[k] = CopyPair{src_pages[i + k], dst_pages[i + k], n};
-      most = std::max(most, n);
-    }
-    if (most == 0) continue;
-    for (int32_t j = 0; j < num_caches; j += kMaxCaches) {
-      c.num_caches = std::min(kMaxCaches, num_caches - j);
-      for (int32_t k = 0; k < c.num_caches; ++k) c.caches[k] = caches[j + k];
-      if (launch_copy_pages(c, most, s) != cudaSuccess) return MLA_ERR_CUDA;
-    }
-  }
-  return MLA_OK;
+  if (num_pairs <= CopyParamsSmall::max_pairs && num_caches <= CopyParamsSmall::max_caches)
+    return copy_pages<CopyParamsSmall>(*dims, src_pages, dst_pages, num_tokens, num_pairs, caches, num_caches, s);
+  return copy_pages<CopyParamsLarge>(*dims, src_pages, dst_pages, num_tokens, num_pairs, caches, num_caches, s);
 }
 
 mla_status mla_run(mla_plan_t p, const void* q_nope, const void* q_pe, const void* cache, void* out, float* lse,

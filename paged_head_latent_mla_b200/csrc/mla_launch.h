@@ -116,13 +116,19 @@ struct CopyPair {
   int32_t bytes;  // a multiple of the cache row's size
 };
 constexpr int32_t kMaxCopyPairs = 1024;
+// Both lists travel as kernel parameters, and a launch pays for the parameters' size, so
+// the few pairs of a fork have a smaller form.
+template <int32_t kPairs, int32_t kCaches>
 struct CopyParams {
+  static constexpr int32_t max_pairs = kPairs, max_caches = kCaches;
   int64_t page_bytes;
   int32_t num_pairs;
   int32_t num_caches;
-  void* caches[kMaxCaches];
-  CopyPair pairs[kMaxCopyPairs];
+  void* caches[kCaches];
+  CopyPair pairs[kPairs];
 };
+using CopyParamsSmall = CopyParams<64, 64>;  // 1.3 KB
+using CopyParamsLarge = CopyParams<kMaxCopyPairs, kMaxCaches>;  // 13 KB
 
 // cudaErrorInvalidValue when a tensor map cannot be encoded.
 cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream);
@@ -132,6 +138,7 @@ cudaError_t launch_merge_state(const MergeStateParams& p, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyParams& p, int rows, bool bf16, int num_sms, cudaStream_t stream);
 cudaError_t launch_compact(const CompactParams& p, int rows, cudaStream_t stream);
 // max_bytes: the largest pair of the launch
-cudaError_t launch_copy_pages(const CopyParams& p, int32_t max_bytes, cudaStream_t stream);
+template <typename Params>
+cudaError_t launch_copy_pages(const Params& p, int32_t max_bytes, cudaStream_t stream);
 
 }  // namespace mla

@@ -551,7 +551,8 @@ __global__ void __launch_bounds__(kCompactThreads) mla_compact_kernel(const __gr
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPart = kCopyThreads * 16 * 4;
 
-__global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(const __grid_constant__ CopyParams p) {
+template <typename Params>
+__global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(const __grid_constant__ Params p) {
   const CopyPair pr = p.pairs[blockIdx.y];
   const int off = blockIdx.x * kCopyPart;
   if (off >= pr.bytes) return;
@@ -611,11 +612,14 @@ cudaError_t launch_compact(const CompactParams& p, int rows, cudaStream_t stream
   return cudaGetLastError();
 }
 
-cudaError_t launch_copy_pages(const CopyParams& p, int32_t max_bytes, cudaStream_t stream) {
+template <typename Params>
+cudaError_t launch_copy_pages(const Params& p, int32_t max_bytes, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((max_bytes + kCopyPart - 1) / kCopyPart), static_cast<unsigned>(p.num_pairs),
                   static_cast<unsigned>(p.num_caches));
   mla_copy_pages_kernel<<<grid, kCopyThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
+template cudaError_t launch_copy_pages(const CopyParamsSmall&, int32_t, cudaStream_t);
+template cudaError_t launch_copy_pages(const CopyParamsLarge&, int32_t, cudaStream_t);
 
 }  // namespace mla
