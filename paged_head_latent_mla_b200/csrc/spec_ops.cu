@@ -182,23 +182,31 @@ struct RowPass {
   }
   // What is left of (clean) chunk c's weights; kQ: a child was rejected.
   template <bool kQ>
-  __device__ __forceinline__ void weights(const Chunk<T, kVec>& cp, const Chunk<T, kVec>& cq, int c,
+  __device__ __forceinline__ void weights(const Chunk<T, kVec>& cp, const Chunk<T, kVec>& cq,
                                           double (&w)[kVec]) const {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       w[i] = static_cast<double>(cp.get(i));
       if (kQ) w[i] = left_of(w[i], static_cast<double>(cq.get(i)), S);
     }
-    if (!kDraft) {
-      const int e0 = c * kVec - head;
+  }
+  // Point masses: the first chunk of c, c + step, ... (below hi) that holds a rejected
+  // token.  Looked up once and again behind every such chunk, not for each chunk.
+  __device__ int zero_chunk(int c, int step, int hi) const {
+    int best = hi;
+    if (!kDraft)
       for (int k = 0; k < rejected; ++k) {
-        const int at = zero[k] - e0;
-        if (static_cast<unsigned>(at) < static_cast<unsigned>(kVec)) {
-#pragma unroll
-          for (int i = 0; i < kVec; ++i)
-            if (at == i) w[i] = 0.0;
-        }
+        if (zero[k] >= V) continue;
+        const int at = (zero[k] + head) / kVec;
+        if (at >= c && at < best && ((at - c) & (step - 1)) == 0) best = at;
       }
+    return best;
+  }
+  __device__ void clear_zeros(int c, double (&w)[kVec]) const {
+    for (int k = 0; k < rejected; ++k) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (zero[k] == c * kVec - head + i) w[i] = 0.0;
     }
   }
   // Sum over chunks lo + lane, lo + lane + 32, ...: kBatch chunks' loads in flight.
@@ -206,6 +214,7 @@ struct RowPass {
   __device__ __forceinline__ double sum(int lo, int hi, int lane) const {
     constexpr int kAcc = kVec > 1 ? 4 : 1;
     double acc[kAcc] = {};
+    int special = kDraft ? hi : zero_chunk(lo + lane, 32, hi);
     for (int c0 = lo + lane; c0 < hi; c0 += 32 * kBatch) {
       Chunk<T, kVec> cp[kBatch], cq[kQ ? kBatch : 1];
 #pragma unroll
@@ -227,7 +236,11 @@ struct RowPass {
           if (kQ) q0.clean();
         }
         double w[kVec];
-        weights<kQ>(cp[k], q0, c0 + 32 * k, w);
+        weights<kQ>(cp[k], q0, w);
+        if (!kDraft && c0 + 32 * k == special) {
+          clear_zeros(special, w);
+          special = zero_chunk(special + 32, 32, hi);
+        }
 #pragma unroll
         for (int i = 0; i < kVec; ++i) acc[i % kAcc] += w[i];
       }
@@ -460,9 +473,10 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
     cq.clean();
     double w[kVec];
     if (kDraft && rejected > 0)
-      rp.template weights<kDraft>(cp, cq, c, w);
+      rp.template weights<kDraft>(cp, cq, w);
     else
-      rp.template weights<false>(cp, cq, c, w);
+      rp.template weights<false>(cp, cq, w);
+    if (!kDraft) rp.clear_zeros(c, w);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) sum += w[i];
