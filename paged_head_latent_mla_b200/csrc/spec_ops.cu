@@ -84,11 +84,7 @@ struct Chunk {
     const int e0 = c * kVec - head;
     if (kVec > 1) {
       if (e0 >= 0 && e0 + kVec <= V) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + e0));
-        r[0] = x.x;
-        r[1 % (kVec > 1 ? 4 : 1)] = x.y;
-        r[2 % (kVec > 1 ? 4 : 1)] = x.z;
-        r[3 % (kVec > 1 ? 4 : 1)] = x.w;
+        load_whole(row + e0);
         return;
       }
       clear();
@@ -97,6 +93,19 @@ struct Chunk {
     } else {
       clear();
       if (e0 < V) put(0, row[e0]);
+    }
+  }
+  // All of a chunk's elements exist; a 16-byte chunk is aligned.
+  __device__ __forceinline__ void load_whole(const T* at) {
+    if (kVec > 1) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+      r[0] = x.x;
+      r[1 % (kVec > 1 ? 4 : 1)] = x.y;
+      r[2 % (kVec > 1 ? 4 : 1)] = x.z;
+      r[3 % (kVec > 1 ? 4 : 1)] = x.w;
+    } else {
+      clear();
+      put(0, *at);
     }
   }
   __device__ __forceinline__ void clear() {
@@ -209,42 +218,80 @@ struct RowPass {
         if (zero[k] == c * kVec - head + i) w[i] = 0.0;
     }
   }
-  // Sum over chunks lo + lane, lo + lane + 32, ...: kBatch chunks' loads in flight.
+  // The warp's sum over chunks [lo, hi): batches of 32 * kBatch whole chunks with all their
+  // loads in flight, then single ones, then the row's ragged ends.
   template <int kBatch, bool kQ>
   __device__ __forceinline__ double sum(int lo, int hi, int lane) const {
+    using C = Chunk<T, kVec>;
     constexpr int kAcc = kVec > 1 ? 4 : 1;
     double acc[kAcc] = {};
-    int special = kDraft ? hi : zero_chunk(lo + lane, 32, hi);
-    for (int c0 = lo + lane; c0 < hi; c0 += 32 * kBatch) {
-      Chunk<T, kVec> cp[kBatch], cq[kQ ? kBatch : 1];
+    const int first = max(lo, head > 0 ? 1 : 0), end = min(hi, (V + head) / kVec);  // whole chunks
+    int special = kDraft ? hi : zero_chunk(first + lane, 32, end);
+    auto add = [&](C& cp, C& cq, int c) {
+      if (!kDraft && c == special) {
+        double w[kVec];
+        cp.clean();
+        weights<false>(cp, cq, w);
+        clear_zeros(c, w);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int c = c0 + 32 * k;
-        if (c < hi) {
-          cp[k].load(p, head, c, V);
-          if (kQ) cq[kQ ? k : 0].load(q, head, c, V);
-        } else {
-          cp[k].clear();
-          if (kQ) cq[kQ ? k : 0].clear();
-        }
+        for (int i = 0; i < kVec; ++i) acc[i % kAcc] += w[i];
+        special = zero_chunk(c + 32, 32, end);
+        return;
+      }
+      if ((cp.bits() | (kQ ? cq.bits() : 0u)) & C::kOddBits) {
+        cp.clean();
+        if (kQ) cq.clean();
       }
 #pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const double p1 = static_cast<double>(cp.get(i));
+        if (kQ) {
+          const double d = __fma_rn(-S, static_cast<double>(cq.get(i)), p1);
+          if (d > 0.0) acc[i % kAcc] += d;  // (one predicated addition)
+        } else {
+          acc[i % kAcc] += p1;
+        }
+      }
+    };
+    const T* p0 = p + (static_cast<int64_t>(first + lane) * kVec - head);
+    const T* q0 = kQ ? q + (static_cast<int64_t>(first + lane) * kVec - head) : nullptr;
+    int b = first;
+    for (; b + 32 * kBatch <= end; b += 32 * kBatch, p0 += 32 * kBatch * kVec, q0 += kQ ? 32 * kBatch * kVec : 0) {
+      C cp[kBatch], cq[kQ ? kBatch : 1];
+#pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        Chunk<T, kVec>& q0 = cq[kQ ? k : 0];
-        if ((cp[k].bits() | (kQ ? q0.bits() : 0u)) & Chunk<T, kVec>::kOddBits) {
-          cp[k].clean();
-          if (kQ) q0.clean();
+        cp[k].load_whole(p0 + 32 * k * kVec);
+        if (kQ) cq[kQ ? k : 0].load_whole(q0 + 32 * k * kVec);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) add(cp[k], cq[kQ ? k : 0], b + lane + 32 * k);
+    }
+#pragma unroll 1
+    for (int c = b + lane; c < end; c += 32, p0 += 32 * kVec, q0 += kQ ? 32 * kVec : 0) {
+      C cp, cq;
+      cp.load_whole(p0);
+      if (kQ) cq.load_whole(q0);
+      add(cp, cq, c);
+    }
+    if (kVec > 1 && lane < 2) {  // the row's first chunk where it is ragged, and its last
+      const int c = lane == 0 ? 0 : (V + head) / kVec;
+      if (c >= lo && c < hi && (lane == 0 ? head > 0 : c > 0 || head == 0)) {
+        C cp, cq;
+        cp.load(p, head, c, V);
+        cp.clean();
+        cq.clear();
+        if (kQ) {
+          cq.load(q, head, c, V);
+          cq.clean();
         }
         double w[kVec];
-        weights<kQ>(cp[k], q0, w);
-        if (!kDraft && c0 + 32 * k == special) {
-          clear_zeros(special, w);
-          special = zero_chunk(special + 32, 32, hi);
-        }
+        weights<kQ>(cp, cq, w);
+        if (!kDraft) clear_zeros(c, w);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) acc[i % kAcc] += w[i];
       }
     }
+    __syncwarp();
     double t = acc[0];
     if (kAcc == 4) t = (acc[0] + acc[1 % kAcc]) + (acc[2 % kAcc] + acc[3 % kAcc]);
 #pragma unroll
@@ -342,60 +389,45 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
   const int per = (segs + 31) / 32;  // segments of a lane, in order
   int flip = 0;                      // the buffer of the last pass's sums
 
-  // One pass over node v's row of weights by the whole cluster; afterwards s.seg[flip]
-  // holds every warp's sum in every block, and the return value is their total.
-  auto run_pass = [&](int v, int rejected, double S) -> double {
-    if (!kDraft) __syncthreads();  // the list of rejections is written
-    flip ^= 1;
-    const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, S, s, C);
-    int lo, hi;
-    rp.segment(rank, warp, &lo, &hi);
-    double t;
-    if (kDraft && rejected > 0)
-      t = rp.template sum<(kVec > 4 ? 2 : 4), kDraft>(lo, hi, lane);
-    else
-      t = rp.template sum<(kVec > 1 ? 4 : 8), false>(lo, hi, lane);
-    if (lane < static_cast<int>(C))
-      st_cluster_f64(ptx::map_to_cta(ptx::smem_addr(&s.seg[flip][rank * kVWarps + warp]), lane), t);
-    __syncwarp();
-    cluster_sync();
-    double mine = 0.0;
-    for (int i = 0; i < per; ++i)
-      if (lane * per + i < segs) mine += s.seg[flip][lane * per + i];
-    return __shfl_sync(0xffffffffu, warp_scan(mine, lane), 31);
-  };
-
   // ---------------------------------------------------------------- walk (all blocks alike)
-  int v = 0, kept = 1, rejected = 0;
-  double S = 0.0;  // draft: the sum of the rejections' Z
+  // Children are tried until one is accepted (its children are next), a pass has to give
+  // the next Z, or none is left and a pass gives the sum W of what is left.  One place calls
+  // for all passes: copies of that code would evict one another from the instruction cache.
+  int v = 0, c = s.node[0].first, kept = 1, rejected = 0;
+  double S = 0.0, Z = 1.0, W;  // S: the sum of the rejections' Z (draft)
   while (true) {
-    int c = s.node[v].first, got = -1;
-    double Z = 1.0;
-    rejected = 0;
-    S = 0.0;
-    for (; c >= 0; c = s.node[c].next) {
+    while (c >= 0) {
       const WalkNode nd = s.node[c];
-      if (nd.tok < 0) {  // given
-        got = c;
-        break;
-      }
+      bool accept = nd.tok < 0;  // given
       double w = nd.p;
-      if (kDraft) {
-        w = left_of(w, nd.q, S);
-      } else {
-        for (int k = 0; k < rejected; ++k)
-          if (s.zero[k] == nd.tok) w = 0.0;
+      if (!accept) {
+        const double u = nd.u;
+        double limit;
+        if (kDraft) {
+          w = left_of(w, nd.q, S);
+          limit = __dmul_rn(__dmul_rn(u, static_cast<double>(nd.q)), Z);
+        } else {
+          for (int k = 0; k < rejected; ++k)
+            if (s.zero[k] == nd.tok) w = 0.0;
+          limit = __dmul_rn(u, Z);
+        }
+        accept = limit < w;
       }
-      const double u = nd.u;
-      const double limit = kDraft ? __dmul_rn(__dmul_rn(u, static_cast<double>(nd.q)), Z) : __dmul_rn(u, Z);
-      if (limit < w) {
-        got = c;
-        break;
+      if (accept) {
+        v = c;
+        if (rank == 0 && tid == 0) a.accept_index[t0 + kept] = v;
+        ++kept;
+        c = s.node[v].first;
+        rejected = 0;
+        S = 0.0;
+        Z = 1.0;
+        continue;
       }
       ++rejected;
+      c = nd.next;
       if (kDraft) {
         S += Z;
-        if (nd.next >= 0) Z = run_pass(v, rejected, S);
+        if (c >= 0) break;  // its Z
       } else {
         __syncthreads();  // all have read the list
         if (tid == 0) s.zero[rejected - 1] = nd.tok;
@@ -403,16 +435,35 @@ __global__ void __launch_bounds__(kVThreads, kVBlocksPerSm) mla_verify_kernel(co
         __syncthreads();
       }
     }
-    if (got < 0) break;
-    v = got;
-    if (rank == 0 && tid == 0) a.accept_index[t0 + kept] = v;
-    ++kept;
-  }
 
-  double W = run_pass(v, rejected, S);
-  if (!(W > 0.0) && rejected > 0) {
-    rejected = 0;
-    W = run_pass(v, 0, 0.0);
+    // a pass over node v's row of weights by the whole cluster: every warp's sum goes to
+    // all blocks
+    flip ^= 1;
+    {
+      const RowPass<T, kVec, kDraft> rp(a, t0 + v, rejected, S, s, C);
+      int lo, hi;
+      rp.segment(rank, warp, &lo, &hi);
+      double t;
+      if (kDraft && rejected > 0)
+        t = rp.template sum<(kVec > 4 ? 2 : 4), kDraft>(lo, hi, lane);
+      else
+        t = rp.template sum<(kVec > 1 ? 4 : 8), false>(lo, hi, lane);
+      if (lane < static_cast<int>(C))
+        st_cluster_f64(ptx::map_to_cta(ptx::smem_addr(&s.seg[flip][rank * kVWarps + warp]), lane), t);
+      __syncwarp();
+      cluster_sync();
+    }
+    double mine = 0.0;
+    for (int i = 0; i < per; ++i)
+      if (lane * per + i < segs) mine += s.seg[flip][lane * per + i];
+    W = __shfl_sync(0xffffffffu, warp_scan(mine, lane), 31);
+    if (c >= 0) {
+      Z = W;
+      continue;
+    }
+    if (W > 0.0 || rejected == 0) break;
+    rejected = 0;  // the rejections left nothing: p itself
+    S = 0.0;
   }
   if (rank == 0 && tid == 0) a.num_accepted[b] = kept;
   if (!(W > 0.0)) {
