@@ -156,6 +156,28 @@ def test_masked_rows_may_hold_anything(H, bad, where):
         assert torch.isnan(lb[sees]).all()
 
 
+def test_masked_rows_may_hold_anything_with_split_keys():
+    """The same where every key tile is an item of its own and the partial results merge."""
+    n, ctx = 90, 130
+    tree = [-1] + [(i - 1) // 2 for i in range(1, n)]
+    d = make_custom([n], [n + ctx], 32, 16, seed=22)
+    odd = [7, 40, 88]
+    sees = [i for i in range(n) if set(S.path_of(tree, i)) & set(odd)]
+    free = [i for i in range(n) if i not in sees]
+    hurt = d.cache.clone()
+    for a in odd:
+        page, slot = O.key_location(d.kv_indptr, d.kv_indices, 16, 0, ctx + a)
+        hurt[page, slot] = float("nan")
+    plan = tree_plan(d, tree, split_keys=64)
+    assert M.mla_plan_get_info(plan)["num_merge"] > 0
+    args = (d.q_nope.to(DEV), d.q_pe.to(DEV))
+    a, la = M.mla_run(plan, *args, d.cache.to(DEV), return_lse=True)
+    b, lb = M.mla_run(plan, *args, hurt.to(DEV), return_lse=True)
+    assert M.mla_plan_check(plan) == M.MLA_OK
+    assert torch.equal(a[free], b[free]) and torch.equal(la[free], lb[free])
+    assert torch.isnan(lb[sees]).all() and torch.isnan(b[sees]).all()
+
+
 def test_cascade_of_trees_matches_oracle():
     rng = np.random.default_rng(31)
     q = [4, 4, 4, 4, 3, 4]
@@ -271,6 +293,44 @@ def test_verify_batches(batch):
                         rng.random(batch, dtype=np.float32))
     if batch > 1:
         assert (want[1] > 1).any() and (want[2][want[1] > 0] >= 0).all()
+
+
+def test_verify_a_large_vocabulary():
+    rng = np.random.default_rng(14)
+    q = [9] * 40
+    trees = [[-1, 0, 0, 0, 1, 1, 4, 4, 4] for _ in q]
+    plan, d = verify_plan(q, trees)
+    p, r = peaked(rng, 360, 131071, torch.float32)
+    want = check_verify(plan, d, trees, drafted(rng, d, trees, r), p, r, rng.random(360, dtype=np.float32),
+                        rng.random(40, dtype=np.float32))
+    assert (want[1] > 2).any()
+
+
+def test_verify_on_two_streams_at_once():
+    """Two calls on one plan, each with its own outputs, running side by side."""
+    rng = np.random.default_rng(15)
+    q = [9] * 30
+    trees = [random_tree(rng, 9, roots=1) for _ in q]
+    plan, d = verify_plan(q, trees)
+    p, r = peaked(rng, 270, 20000, torch.float32)
+    tok = drafted(rng, d, trees, r)
+    dev = [x.to(DEV) for x in (p, r, torch.from_numpy(tok))]
+    u = [rng.random(270, dtype=np.float32) for _ in range(2)]
+    un = [rng.random(30, dtype=np.float32) for _ in range(2)]
+    ud = [(torch.from_numpy(a).to(DEV), torch.from_numpy(b).to(DEV)) for a, b in zip(u, un)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(M.mla_verify_tree(plan, dev[2], dev[0], *ud[i], draft_probs=dev[1]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        want = S.verify_tree(d.qo_indptr, flat(trees), tok, p.double().numpy(), u[i], un[i], r.double().numpy())
+        for g in got[i]:
+            for a, b in zip(g, want):
+                assert np.array_equal(a.cpu().numpy(), b)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
