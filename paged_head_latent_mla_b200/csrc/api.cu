@@ -515,6 +515,7 @@ mla_status attention_launch_of(mla_plan_t p, const void* q_nope, const void* q_p
   a->cache_rows = static_cast<uint64_t>(p->dims.num_pages) * p->dims.page_size;
   a->num_work = static_cast<int>(p->sz.cap_work);
   a->wait_prior_grid = false;
+  a->few_rows = p->tree && p->layout.max_nodes * p->dims.num_heads <= kTileM - 32;
   return MLA_OK;
 }
 

@@ -163,7 +163,10 @@ __device__ __noinline__ void clear_non_finite(uint8_t* stage, int lane) {
 //   softmax  : S(j) = ours + peer's; mask, online softmax, P(j) -> P[j % 2]
 //   PV warp  : PV(j): O += P[j % 2] . V(stage j % 3), as soon as P(j) is written
 // kTree: the step's rows are trees of drafted tokens, masked by the plan's words.
-template <bool kTree>
+// kPace: in an item with idle lane quarters (no rows), their exchange and softmax warps only
+// keep pace: nobody needs their scores, and the pair's link is left to the quarters that
+// have rows.
+template <bool kTree, bool kPace>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
     mla_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                     const __grid_constant__ CUtensorMap tm_kpe, const AttnParams p) {
@@ -388,7 +391,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const uint32_t xq_peer = map_to_cta(sb + kX + q * 8192 + lane * 16, peer);
     const uint32_t xfull_peer = map_to_cta(bar(bXFull + q), peer);
-    for (int j = 0; j < ntiles; ++j) {
+    const int pushed = kPace && 32 * q >= w.n_rows ? 0 : ntiles;
+    for (int j = pushed; kPace && j < ntiles; ++j) {
+      if (!wait_warp(bar(bSFull + (j & 1)), (j >> 1) & 1, kSiteExchange, false)) break;
+      if (lane == 0) mbar_arrive(bar(bSEmpty + (j & 1)));
+    }
+    for (int j = 0; j < pushed; ++j) {
       const int b2 = j & 1;
       if (!wait_warp(bar(bSFull + b2), (j >> 1) & 1, kSiteExchange, false)) break;
       tc_fence_after();
@@ -415,9 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * q) << 16);
     int vis = w.diag_base + r / p.num_heads + 1;
     vis = max(0, min(vis, w.kv_len));
-    // Rows past the tile's last: their results are not written.  A tree step lets them see
-    // every key, so that they cost no masking (their P rows reach no other row of O).
-    if (r >= w.n_rows) vis = kTree ? w.kv_len : 0;
+    // Rows past the tile's last see every key, so that they cost no masking: their results
+    // are not written, and their P rows reach no other row of O.
+    if (r >= w.n_rows) vis = w.kv_len;
     const int lim = min(vis, w.key_end);  // keys < lim are visible in this chunk
     const float* xq_ptr = reinterpret_cast<const float*>(smem + kX + q * 8192 + lane * 16);
     const float scale = p.scale_log2;  // > 0 (the planner rejects other scales)
@@ -472,6 +480,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
       if (lane == 0) mbar_arrive(bar(bQTmem));
     }
 
+    if (kPace && 32 * q >= w.n_rows) {  // (its P rows are never written, nor its O rows read)
+      for (int j = 0; ok && j < ntiles; ++j) {
+        const int b2 = j & 1;
+        if (!(ok = wait_warp(bar(bSFull + b2), (j >> 1) & 1, kSiteSoftS, false))) break;
+        if (lane == 0) mbar_arrive(bar(bSEmpty + b2));
+        if (j >= 2 && !(ok = wait_warp(bar(bPVDone + b2), ((j >> 1) - 1) & 1, kSiteSoftPV, false))) break;
+        if (lane == 0) mbar_arrive(bar(bPFull + b2));
+      }
+      ok = false;  // nothing to write
+    }
     for (int j = 0; ok && j < ntiles; ++j) {
       const int b2 = j & 1;
       // (fetched during the wait for S(j); a register held from here on would spill)
@@ -790,7 +808,7 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (configured_device != dev) {
-    for (auto k : {mla_attn_kernel<false>, mla_attn_kernel<true>}) {
+    for (auto k : {mla_attn_kernel<false, true>, mla_attn_kernel<true, false>, mla_attn_kernel<true, true>}) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(attn::kSmemAlloc));
       if (e != cudaSuccess) return e;
     }
@@ -814,7 +832,12 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   } else {
     tm_kpe = tm_kv;
   }
-  const auto kernel = p.tree_items != nullptr ? mla_attn_kernel<true> : mla_attn_kernel<false>;
+  // A tree step paces its idle quarters where its items have them throughout: 64 rows of one
+  // node, 64 heads, 4096 keys 112 -> 103 us; a step of full items keeps the tile loop that
+  // the compiler makes without that code (4 rows of 257 nodes, 64 heads: 590 against 636 us).
+  const auto kernel = p.tree_items == nullptr ? mla_attn_kernel<false, true>
+                      : a.few_rows            ? mla_attn_kernel<true, true>
+                                              : mla_attn_kernel<true, false>;
   if (!a.wait_prior_grid) {
     kernel<<<2 * a.num_work, attn::kThreads, attn::kSmemAlloc, stream>>>(tm_q, tm_kv, tm_kpe, p);
     return cudaGetLastError();

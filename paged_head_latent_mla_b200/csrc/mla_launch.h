@@ -47,6 +47,7 @@ struct AttnLaunch {
   int num_work;         // launch slots (CTA pairs)
   bool wait_prior_grid; // launched as a programmatic dependent of the previous kernel
                         // (an append): the key loads wait for that grid's writes
+  bool few_rows = false;  // every batch row's queries leave lane quarters of a tile idle
 };
 
 struct MergeParams {
