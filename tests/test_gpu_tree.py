@@ -375,6 +375,25 @@ def test_verify_borders_are_exact(draft):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("scale", [2.0 ** -133, 2.0 ** -120, 2.0, 2.0 ** 100, 2.0 ** 125])
+def test_verify_weights_of_any_size(dtype, draft, scale):
+    """Weights need not sum to 1: small whole numbers times a power of two, down to the
+    types' subnormals (bf16's smallest is 2^-133) and up to near their largest."""
+    rng = np.random.default_rng(3)
+    q = [5] * 60
+    trees = [random_tree(rng, 5, roots=1) for _ in q]
+    plan, d = verify_plan(q, trees)
+    T, V = d.total_tokens, 37
+    p = (torch.from_numpy(rng.integers(0, 4, (T, V))).double() * scale).to(dtype)
+    r = (torch.from_numpy(rng.integers(0, 4, (T, V))).double() * scale).to(dtype)
+    assert torch.equal(p.double() / scale, (p.double() / scale).round()) and p.any()
+    tok = rng.integers(0, V, T).astype(np.int32)
+    check_verify(plan, d, trees, tok, p, r if draft else None, rng.random(T, dtype=np.float32),
+                 rng.random(60, dtype=np.float32))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("draft", [True, False])
 def test_verify_odd_weights(dtype, draft):
     """Zero rows, infinities, NaN and negative weights, given tokens, tokens out of range,
     the same token drafted twice."""
