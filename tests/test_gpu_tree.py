@@ -189,10 +189,14 @@ def test_cascade_of_trees_matches_oracle():
     check_attention(out, lse, ref)
 
 
-def test_tree_graph_replays_updated_steps():
+@pytest.mark.parametrize("first", [0, 2])
+def test_tree_graph_replays_updated_steps(first):
+    """Captured on one step, replayed on others: more and fewer rows, nodes and keys (the
+    step captured second has idle lane quarters only)."""
     rng = np.random.default_rng(41)
     TM, H, P = 40, 32, 32
     specs = [([5, 9, 1], [60, 300, 1]), ([40], [1500]), ([0, 3], [20, 3]), ([8] * 5, [100, 8, 200, 3000, 64])]
+    specs = specs[first:] + specs[:first]
     steps = [make_custom(q, k, H, P, seed=43 + i, pool_pages=200) for i, (q, k) in enumerate(specs)]
     trees = [flat([random_tree(rng, n) for n in q]) for q, _ in specs]
     plan = tree_plan(steps[0], trees[0], graph_max_batch=6, graph_max_tokens=TM, graph_max_page_ids=200)
@@ -225,6 +229,23 @@ def test_tree_graph_replays_updated_steps():
         assert (out[T:] == 7.0).all()  # rows behind the step's last are left as they were
     del g
     plan.destroy()
+
+
+@pytest.mark.parametrize("n", [2, 30])
+def test_a_wait_that_runs_out_is_reported(n):
+    """The first key load is never issued (a planning flag): the waits on it run out, the
+    plan reports it, and another plan runs afterwards."""
+    d = make_custom([n, n], [n + 300, n + 40], 32, 64, seed=6)
+    tree = [-1] + [(i - 1) // 2 for i in range(1, n)]
+    args = (d.q_nope.to(DEV), d.q_pe.to(DEV), d.cache.to(DEV))
+    plan = M.mla_plan_tree(*tables(d), np.asarray(tree * 2, dtype=np.int32), num_heads=32, page_size=64,
+                           num_pages=d.num_pages, sm_scale=d.sm_scale, wait_timeout_ns=100_000_000,
+                           debug_flags=M.MLA_DEBUG_DROP_FIRST_KV_LOAD)
+    M.mla_run(plan, *args)
+    assert M.mla_plan_check(plan) == M.MLA_ERR_DEVICE_TIMEOUT
+    plan.destroy()
+    out, lse, _, ref = run_tree(d, tree * 2)
+    check_attention(out, lse, ref)
 
 
 # ------------------------------------------------------------------ verification
@@ -599,7 +620,8 @@ def test_copy_pages_is_bit_exact(P, rope, layers, pairs, part):
     g = torch.Generator().manual_seed(5)
     cache = torch.randint(-2 ** 15, 2 ** 15, (layers, pool, P, 512 + rope), dtype=torch.int16, generator=g)
     dev = cache.to(DEV).view(torch.bfloat16)
-    M.mla_copy_pages(src, dst, dev, num_tokens=n)
+    M.mla_copy_pages(torch.from_numpy(src), dst.tolist(), list(dev.unbind(0)) if layers == 2 else dev, num_tokens=n)
+    M.mla_copy_pages(src, dst, [], num_tokens=n)
     got = dev.view(torch.int16).cpu().numpy()
     for i in range(layers):
         assert np.array_equal(got[i], S.copy_pages(cache[i].numpy(), src, dst, n))
