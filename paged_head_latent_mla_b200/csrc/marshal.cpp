@@ -109,8 +109,20 @@ PyObject* py_tensor(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// rows(t, name, type, dev, tokens, vocab) -> (address, pitch) of a matrix whose rows are
-// contiguous and do not overlap
+// (address, pitch) of a checked [T, V] matrix whose rows must be contiguous and apart, or
+// with the vocabulary and the type where `more`.
+PyObject* matrix(const at::Tensor& t, const char* name, int64_t T, int64_t V, int more) {
+  if (t.dim() != 2 || t.size(0) != T || t.size(1) != V)
+    return value_error(std::string(name) + " must have shape " + text({T, V}) + ", got " + text(t.sizes()));
+  if ((V > 1 && t.stride(1) != 1) || (T > 1 && t.stride(0) < V))
+    return value_error(std::string(name) + " must have contiguous rows");
+  const unsigned long long at = reinterpret_cast<uintptr_t>(t.data_ptr());
+  const long long pitch = T > 1 ? t.stride(0) : V;
+  if (more >= 0) return Py_BuildValue("(KLLi)", at, pitch, static_cast<long long>(V), more);
+  return Py_BuildValue("(KL)", at, pitch);
+}
+
+// rows(t, name, type, dev, tokens, vocab) -> (address, pitch)
 PyObject* py_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (!arity(n, 6)) return nullptr;
@@ -119,14 +131,27 @@ PyObject* py_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!name || !integer(a[2], &type) || !integer(a[3], &dev) || !integer(a[4], &T) || !integer(a[5], &V))
       return nullptr;
     const at::Tensor* t = cuda_tensor(a[0], name, type, dev);
-    if (!t) return nullptr;
-    if (t->dim() != 2 || t->size(0) != T || t->size(1) != V)
-      return value_error(std::string(name) + " must have shape " + text({T, V}) + ", got " + text(t->sizes()));
-    if ((V > 1 && t->stride(1) != 1) || (T > 1 && t->stride(0) < V))
-      return value_error(std::string(name) + " must have contiguous rows");
-    PyObject* at = address_of(*t);
-    if (!at) return nullptr;
-    return Py_BuildValue("(NL)", at, static_cast<long long>(T > 1 ? t->stride(0) : V));
+    return t ? matrix(*t, name, T, V, -1) : nullptr;
+  });
+}
+
+// probabilities(t, name, dev, tokens) -> (address, pitch, vocab, type) of a float32 or
+// bfloat16 matrix
+PyObject* py_probabilities(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 4)) return nullptr;
+    const char* name = PyUnicode_AsUTF8(a[1]);
+    int64_t dev, T;
+    if (!name || !integer(a[2], &dev) || !integer(a[3], &T)) return nullptr;
+    int type = -1;
+    if (THPVariable_Check(a[0])) {
+      const at::Tensor& t = THPVariable_Unpack(a[0]);
+      if (t.dim() == 2 && t.size(1) > 0)
+        type = t.scalar_type() == at::kBFloat16 ? 0 : t.scalar_type() == at::kFloat ? 1 : -1;
+    }
+    if (type < 0) return value_error(std::string(name) + " must be a [T, vocab] tensor of float32 or bfloat16");
+    const at::Tensor* t = cuda_tensor(a[0], name, type, dev);
+    return t ? matrix(*t, name, T, t->size(1), type) : nullptr;
   });
 }
 
@@ -216,6 +241,35 @@ PyObject* py_empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// empty_parts(type, dev, sizes) -> new one-dimensional tensors, parts of one allocation
+PyObject* py_empty_parts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (!arity(n, 3)) return nullptr;
+    int64_t type, dev, sum = 0, size[8];
+    const Py_ssize_t parts = PyTuple_Size(a[2]);
+    if (!integer(a[0], &type) || !integer(a[1], &dev) || parts < 0) return nullptr;
+    if (parts > 8) return value_error("at most eight parts");
+    for (Py_ssize_t i = 0; i < parts; ++i) {
+      if (!integer(PyTuple_GET_ITEM(a[2], i), &size[i])) return nullptr;
+      sum += size[i];
+    }
+    const at::Tensor all = at::empty({sum}, at::TensorOptions().dtype(kTypes[type]).device(at::kCUDA, dev));
+    PyObject* out = PyTuple_New(parts);
+    int64_t from = 0;
+    for (Py_ssize_t i = 0; out && i < parts; from += size[i++]) {
+      auto impl = all.unsafeGetTensorImpl()->shallow_copy_and_detach(c10::VariableVersion(0), true);
+      impl->set_storage_offset(from);
+      impl->set_sizes_contiguous({size[i]});
+      PyObject* t = THPVariable_Wrap(at::Tensor(std::move(impl)));
+      if (t)
+        PyTuple_SET_ITEM(out, i, t);
+      else
+        Py_CLEAR(out);
+    }
+    return out;
+  });
+}
+
 // device() -> the current CUDA device, -1 on a machine without one
 PyObject* py_device(PyObject*, PyObject*) {
   return guarded([] { return PyLong_FromLong(c10::cuda::device_count() > 0 ? c10::cuda::current_device() : -1); });
@@ -245,6 +299,9 @@ PyMethodDef kMethods[] = {
     {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_rows)), METH_FASTCALL, nullptr},
     {"cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_cache)), METH_FASTCALL, nullptr},
     {"caches", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_caches)), METH_FASTCALL, nullptr},
+    {"probabilities", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_probabilities)), METH_FASTCALL,
+     nullptr},
+    {"empty_parts", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_empty_parts)), METH_FASTCALL, nullptr},
     {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_empty)), METH_FASTCALL, nullptr},
     {"device", py_device, METH_NOARGS, nullptr},
     {"stream", py_stream, METH_O, nullptr},
