@@ -668,17 +668,15 @@ def mla_copy_pages(src_pages, dst_pages, caches, num_tokens=None, stream=None) -
     tok = None if num_tokens is None else _i32(num_tokens)
     if src.ndim != 1 or dst.shape != src.shape or (tok is not None and tok.shape != src.shape):
         raise MlaError(MLA_ERR_INVALID_ARGUMENT, "mla_copy_pages: table lengths")
-    if len(caches) == 0:
-        return
-    shape = caches.shape[-3:] if hasattr(caches, "shape") else getattr(caches[0], "shape", ())
-    if len(shape) != 3:
-        raise ValueError("caches must be [num_pages, page_size, 512 + rope_dim]")
     N = _native()
     dev = N.device()
-    ptrs = N.caches(caches, dev, *shape)
+    pools = N.pools(caches, dev)
+    if pools is None:
+        return
+    ptrs, pages, page, width = pools
     if stream is None:
         stream = N.stream(dev)
-    dims = _Dims(128, KV_LORA_RANK, shape[2] - KV_LORA_RANK, shape[1], shape[0], 1.0)
+    dims = _Dims(128, KV_LORA_RANK, width - KV_LORA_RANK, page, pages, 1.0)
     st = load_library().mla_copy_pages(ctypes.byref(dims), N.address(src), N.address(dst),
                                        None if tok is None else N.address(tok), len(src), ptrs, len(ptrs) // 8,
                                        stream)

@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <cstdint>
 #include <exception>
@@ -190,39 +191,81 @@ PyObject* py_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// caches(c, dev, pages, page, width) -> bytes of the layers' addresses; c is a sequence of
-// caches, one cache, or one tensor with a leading layer dimension.
+// Addresses of the layers' caches: `o` is a sequence of caches, one cache, or one tensor
+// with a leading layer dimension.
+PyObject* cache_addresses(PyObject* o, const CacheShape& want) {
+  if (THPVariable_Check(o)) {
+    const int64_t dims = THPVariable_Unpack(o).dim() == 4 ? 4 : 3;
+    const at::Tensor* t = want.check(o, dims);
+    if (!t) return nullptr;
+    const int64_t layers = dims == 4 ? t->size(0) : 1;
+    PyObject* out = PyBytes_FromStringAndSize(nullptr, layers * 8);
+    if (!out) return nullptr;
+    uint64_t* p = reinterpret_cast<uint64_t*>(PyBytes_AS_STRING(out));
+    const uint64_t base = reinterpret_cast<uintptr_t>(t->data_ptr());
+    const uint64_t step = layers > 0 ? static_cast<uint64_t>(t->numel() / layers) * 2 : 0;
+    for (int64_t i = 0; i < layers; ++i) p[i] = base + i * step;
+    return out;
+  }
+  PyObject* seq = PySequence_Fast(o, "caches must be a tensor or a sequence of tensors");
+  if (!seq) return nullptr;
+  const Py_ssize_t layers = PySequence_Fast_GET_SIZE(seq);
+  PyObject* out = PyBytes_FromStringAndSize(nullptr, layers * 8);
+  uint64_t* p = out ? reinterpret_cast<uint64_t*>(PyBytes_AS_STRING(out)) : nullptr;
+  for (Py_ssize_t i = 0; out && i < layers; ++i) {
+    const at::Tensor* t = want.check(PySequence_Fast_GET_ITEM(seq, i), 3);
+    if (t)
+      p[i] = reinterpret_cast<uintptr_t>(t->data_ptr());
+    else
+      Py_CLEAR(out);
+  }
+  Py_DECREF(seq);
+  return out;
+}
+
+// caches(c, dev, pages, page, width) -> bytes of the layers' addresses
 PyObject* py_caches(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     CacheShape want;
     if (!arity(n, 5) || !want.parse(a + 1)) return nullptr;
-    if (THPVariable_Check(a[0])) {
-      const int64_t dims = THPVariable_Unpack(a[0]).dim() == 4 ? 4 : 3;
-      const at::Tensor* t = want.check(a[0], dims);
-      if (!t) return nullptr;
-      const int64_t layers = dims == 4 ? t->size(0) : 1;
-      PyObject* out = PyBytes_FromStringAndSize(nullptr, layers * 8);
-      if (!out) return nullptr;
-      uint64_t* p = reinterpret_cast<uint64_t*>(PyBytes_AS_STRING(out));
-      const uint64_t base = reinterpret_cast<uintptr_t>(t->data_ptr());
-      const uint64_t step = layers > 0 ? static_cast<uint64_t>(t->numel() / layers) * 2 : 0;
-      for (int64_t i = 0; i < layers; ++i) p[i] = base + i * step;
-      return out;
+    return cache_addresses(a[0], want);
+  });
+}
+
+// pools(c, dev) -> (bytes of the layers' addresses, pages, page, width), by the first
+// cache's shape; None where there is no cache
+PyObject* py_pools(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    CacheShape want;
+    if (!arity(n, 2) || !integer(a[1], &want.dev)) return nullptr;
+    THPObjectPtr held;
+    PyObject* first = a[0];
+    if (!THPVariable_Check(first)) {
+      const Py_ssize_t layers = PySequence_Size(a[0]);
+      if (layers < 0) return nullptr;
+      if (layers == 0) Py_RETURN_NONE;
+      held = PySequence_GetItem(a[0], 0);
+      first = held.get();
+      if (!first) return nullptr;
     }
-    PyObject* seq = PySequence_Fast(a[0], "caches must be a tensor or a sequence of tensors");
-    if (!seq) return nullptr;
-    const Py_ssize_t layers = PySequence_Fast_GET_SIZE(seq);
-    PyObject* out = PyBytes_FromStringAndSize(nullptr, layers * 8);
-    uint64_t* p = out ? reinterpret_cast<uint64_t*>(PyBytes_AS_STRING(out)) : nullptr;
-    for (Py_ssize_t i = 0; out && i < layers; ++i) {
-      const at::Tensor* t = want.check(PySequence_Fast_GET_ITEM(seq, i), 3);
-      if (t)
-        p[i] = reinterpret_cast<uintptr_t>(t->data_ptr());
-      else
-        Py_CLEAR(out);
+    int64_t dims = 0;
+    if (THPVariable_Check(first)) {
+      const at::Tensor& t = THPVariable_Unpack(first);
+      dims = t.dim();
+      if (dims == 3 || (dims == 4 && first == a[0])) {
+        if (dims == 4 && t.size(0) == 0) Py_RETURN_NONE;
+        want.pages = t.size(dims - 3);
+        want.page = t.size(dims - 2);
+        want.width = t.size(dims - 1);
+      } else {
+        dims = 0;
+      }
     }
-    Py_DECREF(seq);
-    return out;
+    if (dims == 0) return value_error("caches must be [num_pages, page_size, 512 + rope_dim]");
+    PyObject* at = cache_addresses(a[0], want);
+    if (!at) return nullptr;
+    return Py_BuildValue("(NLLL)", at, static_cast<long long>(want.pages), static_cast<long long>(want.page),
+                         static_cast<long long>(want.width));
   });
 }
 
@@ -299,6 +342,7 @@ PyMethodDef kMethods[] = {
     {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_rows)), METH_FASTCALL, nullptr},
     {"cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_cache)), METH_FASTCALL, nullptr},
     {"caches", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_caches)), METH_FASTCALL, nullptr},
+    {"pools", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_pools)), METH_FASTCALL, nullptr},
     {"probabilities", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_probabilities)), METH_FASTCALL,
      nullptr},
     {"empty_parts", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_empty_parts)), METH_FASTCALL, nullptr},
