@@ -344,7 +344,7 @@ void size_lists(mla_plan_s* p, const PlanLayout& L, int32_t batch, int64_t n_idx
 // Make sure the pooled device buffers hold the current capacities.  Growing a buffer
 // waits for the plan's last run first (its kernels may still read the old one).
 mla_status reserve_device(mla_plan_s* p) {
-  const size_t ws = static_cast<size_t>(p->sz.cap_ws_rows) * kWsRowBytes;
+  const size_t ws = static_cast<size_t>(p->sz.cap_ws_rows) * ws_row_bytes(p->tree);
   const bool grow_blob = p->sz.blob_bytes > p->blob_cap, grow_ws = ws > p->ws_cap;
   if (!grow_blob && !grow_ws) return MLA_OK;
   if (p->d_blob || p->d_ws) quiesce(p);
@@ -496,8 +496,8 @@ mla_status attention_launch_of(mla_plan_t p, const void* q_nope, const void* q_p
   ap.out = out;
   ap.lse = lse;
   ap.ws_o = p->d_ws;
-  ap.ws_lse = p->d_ws ? reinterpret_cast<float*>(p->d_ws + static_cast<size_t>(p->sz.cap_ws_rows) * kWsRowOBytes)
-                      : nullptr;
+  const size_t lse_at = static_cast<size_t>(p->sz.cap_ws_rows) * ws_row_o_bytes(p->tree);
+  ap.ws_lse = p->d_ws ? reinterpret_cast<float*>(p->d_ws + lse_at) : nullptr;
   ap.status = p->d_status();
   ap.status_mirror = p->h_status;
   ap.scale_log2 = p->dims.sm_scale * 1.4426950408889634f;
@@ -985,7 +985,7 @@ mla_status mla_plan_get_info(mla_plan_t p, mla_plan_info* info) {
   info->num_merge = static_cast<int32_t>(p->layout.merge.size());
   info->num_partials = p->layout.num_partials;
   info->num_sms = p->opts.num_sms;
-  info->workspace_bytes = static_cast<int64_t>(p->layout.ws_rows) * static_cast<int64_t>(kWsRowBytes);
+  info->workspace_bytes = static_cast<int64_t>(p->layout.ws_rows) * static_cast<int64_t>(ws_row_bytes(p->tree));
   info->num_merge_refs = static_cast<int32_t>(p->layout.refs.size());
   info->num_cascade = p->layout.num_cascade;
   info->graph = p->graph ? 1 : 0;

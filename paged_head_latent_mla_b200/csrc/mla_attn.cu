@@ -634,9 +634,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
         tc_fence_after();
       }
       if (ok) {
-        const bool part = w.partial >= 0;  // bf16 partial in the workspace, or the output
-        uint8_t* stage = smem + kKV + q * 16384;  // 32 rows x 512 B
-        for (int cc = 0; cc < 256; cc += 32) {
+        const bool part = w.partial >= 0;  // a partial result in the workspace, or the output
+        // A tree step's partials are fp32 (twice the staging): rounded to bf16 like an
+        // ordinary step's they add as much error as the output's own rounding, 2.7e-3
+        // relative to the exact result against 2.3e-3.
+        const bool wide = kTree && part;
+        uint8_t* stage = smem + kKV + q * (wide ? 32768 : 16384);  // 32 rows x 512 (1024) B
+        for (int cc = 0; wide && cc < 256; cc += 32) {
+          uint32_t o[32];
+          if (ntiles > 0) {
+            tmem_ld32(trow + kColO + cc, o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          uint8_t* row = stage + (lane << 10);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 x;
+            mul_f32x2(x.x, x.y, __uint_as_float(o[4 * i + 0]), __uint_as_float(o[4 * i + 1]), inv_l);
+            mul_f32x2(x.z, x.w, __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]), inv_l);
+            *reinterpret_cast<float4*>(row + ((((cc >> 2) + i) ^ lane) << 4)) = x;
+          }
+        }
+        for (int cc = 0; !wide && cc < 256; cc += 32) {
           uint32_t o[32];
           if (ntiles > 0) {
             tmem_ld32(trow + kColO + cc, o);
@@ -657,7 +678,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
         const int nrows = min(32, w.n_rows - 32 * q);  // rows of this warp inside the tile
         uint8_t* base = part ? static_cast<uint8_t*>(p.ws_o) + static_cast<size_t>(w.partial) * kCkv * 2
                              : static_cast<uint8_t*>(p.out) + static_cast<size_t>(w.q_row0) * kCkv * 2;
-        for (int R = 0; R < nrows; ++R) {
+        for (int R = 0; wide && R < nrows; ++R) {
+          uint8_t* dst = static_cast<uint8_t*>(p.ws_o) +
+                         (static_cast<size_t>(w.partial + 32 * q + R) * kCkv + 256 * rank) * 4 + (lane << 4);
+          const uint8_t* src = stage + (R << 10);
+          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src + ((lane ^ R) << 4));
+          *reinterpret_cast<uint4*>(dst + 512) = *reinterpret_cast<const uint4*>(src + (((lane + 32) ^ R) << 4));
+        }
+        for (int R = 0; !wide && R < nrows; ++R) {
           uint8_t* dst = base + (static_cast<size_t>(32 * q + R) * kCkv + 256 * rank) * 2;
           *reinterpret_cast<uint4*>(dst + (lane << 4)) =
               *reinterpret_cast<const uint4*>(stage + (R << 9) + ((lane ^ R) << 4));
@@ -688,10 +716,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
 // Combine the partials of split (or cascaded) query tiles by their log-sum-exp:
 // M = max_i lse_i, out = sum_i e^{lse_i - M} o_i / sum_i e^{lse_i - M},
 // lse = M + ln sum_i e^{lse_i - M} (FlashInferMLAManager.run: merging key segments).
-// One warp per row; lane l owns columns [16l, 16l + 16), so every load and store of a
-// row is one contiguous 1 KB access.  Up to eight partials are in flight at a time, and
-// a tile with more than 32 partials is merged 32 at a time against a running maximum.
+// One warp per row; lane l owns columns [16l, 16l + 16) of bf16 partials, so every load and
+// store of a row is one contiguous 1 KB access, or columns 128k + [4l, 4l + 4) of a tree
+// step's fp32 ones (kTree).  Up to eight (four) partials are in flight at a time, and a tile
+// with more than 32 partials is merged 32 at a time against a running maximum.
+template <bool kTree>
 __global__ void __launch_bounds__(256) mla_merge_kernel(const MergeParams p) {
+  constexpr int kAtOnce = kTree ? 4 : 8, kPieces = kTree ? 4 : 2;  // of 16 bytes per lane and partial
   // The merge list and the reference list are plan data, written before the attention
   // grid started: read them while that grid drains.
   const MergeItem m = p.merge[blockIdx.x >> 4];  // 16 blocks per split query tile
@@ -714,19 +745,16 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MergeParams p) {
     if (i0 > 0) ref_l = lane < cnt ? refs[i0 + lane] : 0;
     const float l_l = lane < cnt ? p.ws_lse[static_cast<size_t>(ref_l) + r] : neg_inf;
     // every partial of this group in flight before any is used (8 at a time)
-    for (int k = 0; k < cnt; k += 8) {
-      uint4 v[8][2];
+    for (int k = 0; k < cnt; k += kAtOnce) {
+      uint4 v[kAtOnce][kPieces];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kAtOnce; ++u) {
         const int ref_u = __shfl_sync(0xffffffffu, ref_l, (k + u) & 31);
-        if (k + u < cnt) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const uint8_t*>(p.ws_o) + ((static_cast<size_t>(ref_u) + r) * kCkv + 16 * lane) * 2);
-          v[u][0] = src[0];
-          v[u][1] = src[1];
-        } else {
-          v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
-        }
+        const uint4* src = reinterpret_cast<const uint4*>(p.ws_o) +
+                           (static_cast<size_t>(ref_u) + r) * (32 * kPieces) + (kTree ? lane : kPieces * lane);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          v[u][i] = k + u < cnt ? src[kTree ? 32 * i : i] : make_uint4(0u, 0u, 0u, 0u);
       }
       if (k == 0) {
         // the group's running max; earlier groups' sums are rescaled to it
@@ -743,7 +771,7 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MergeParams p) {
         M = Mn;
       }
       // (a tree step's partial that saw a NaN key carries it on, weight and all)
-      const bool counts = M != neg_inf || (p.tree && l_l != l_l);
+      const bool counts = M != neg_inf || (kTree && l_l != l_l);
       const float wl = (lane < cnt && counts) ? __expf(l_l - M) : 0.f;
       if (k == 0) {
         float zg = wl;
@@ -752,27 +780,37 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MergeParams p) {
         z += zg;
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kAtOnce; ++u) {
         const float wk = __shfl_sync(0xffffffffu, wl, (k + u) & 31);
         const uint32_t* wv = reinterpret_cast<const uint32_t*>(v[u]);
+        if (kTree) {
 #pragma unroll
-        for (int k2 = 0; k2 < 8; ++k2) {
-          acc[2 * k2] += wk * __uint_as_float(wv[k2] << 16);
-          acc[2 * k2 + 1] += wk * __uint_as_float(wv[k2] & 0xffff0000u);
+          for (int k2 = 0; k2 < 16; ++k2) acc[k2] += wk * __uint_as_float(wv[k2]);
+        } else {
+#pragma unroll
+          for (int k2 = 0; k2 < 8; ++k2) {
+            acc[2 * k2] += wk * __uint_as_float(wv[k2] << 16);
+            acc[2 * k2 + 1] += wk * __uint_as_float(wv[k2] & 0xffff0000u);
+          }
         }
       }
     }
   }
-  const bool has = z > 0.f || (p.tree && z != z);
+  const bool has = z > 0.f || (kTree && z != z);
   const float inv = has ? 1.f / z : 0.f;
   uint4 o[2];
   uint32_t* ov = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
   for (int k2 = 0; k2 < 8; ++k2) ov[k2] = ptx::pack_bf16x2(acc[2 * k2] * inv, acc[2 * k2 + 1] * inv);
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(m.q_row0 + r) * kCkv +
-                                        16 * lane);
-  dst[0] = o[0];
-  dst[1] = o[1];
+  __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(m.q_row0 + r) * kCkv;
+  if (kTree) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint2*>(row + 128 * i + 4 * lane) = make_uint2(ov[2 * i], ov[2 * i + 1]);
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(row + 16 * lane);
+    dst[0] = o[0];
+    dst[1] = o[1];
+  }
   if (p.lse != nullptr && lane == 0) p.lse[m.q_row0 + r] = has ? M + __logf(z) : neg_inf;
 }
 
@@ -880,7 +918,7 @@ cudaError_t launch_merge(const MergeParams& p, int num_merge, cudaStream_t strea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_merge_kernel, p);
+  return cudaLaunchKernelEx(&cfg, p.tree ? mla_merge_kernel<true> : mla_merge_kernel<false>, p);
 }
 
 }  // namespace mla

@@ -14,10 +14,12 @@ constexpr int kRope = 64;
 constexpr int kTileM = 128;    // query rows per tile (tokens x heads)
 constexpr int kTileN = MLA_KEY_TILE;  // keys per tile (64)
 // Split-KV workspace, addressed by row: each partial result occupies as many rows as
-// its query tile.  All rows' bf16 outputs (512 wide) come first, then all their fp32
-// log-sum-exps.
+// its query tile.  All rows' outputs (512 wide; bf16, of a tree step fp32) come first, then
+// all their fp32 log-sum-exps.
 constexpr size_t kWsRowOBytes = size_t(kCkv) * 2;
 constexpr size_t kWsRowBytes = kWsRowOBytes + 4;
+constexpr size_t ws_row_o_bytes(bool tree) { return tree ? 2 * kWsRowOBytes : kWsRowOBytes; }
+constexpr size_t ws_row_bytes(bool tree) { return ws_row_o_bytes(tree) + 4; }
 
 // One unit of attention work: a query tile of up to 128 rows against keys
 // [key_begin, key_end).  Processed by one CTA pair; field order matches
