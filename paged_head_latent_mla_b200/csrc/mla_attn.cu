@@ -881,9 +881,9 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   } else {
     tm_kpe = tm_kv;
   }
-  // A tree step paces its idle quarters where its items have them throughout: 64 rows of one
-  // node, 64 heads, 4096 keys 112 -> 103 us; a step of full items keeps the tile loop that
-  // the compiler makes without that code (4 rows of 257 nodes, 64 heads: 590 against 636 us).
+  // A tree step paces its idle quarters where its items have them throughout (64 rows of one
+  // node, 64 heads, 4096 keys: 112 us without, 98 with); full items do without that code (4
+  // rows of 257 nodes, 64 heads: 573 us, 578 with it).
   const auto kernel = p.tree_items == nullptr ? mla_attn_kernel<false, true>
                       : a.few_rows            ? mla_attn_kernel<true, true>
                                               : mla_attn_kernel<true, false>;
