@@ -192,10 +192,14 @@ def _native():
         import torch  # noqa: F401  (its libraries must be loaded first)
 
         try:
-            _helpers = importlib.import_module("._marshal", __name__)
+            m = importlib.import_module("._marshal", __name__)
         except ImportError as e:
             raise RuntimeError("the binding's native part is missing or stale: python -m "
                                "paged_head_latent_mla_b200._build --force") from e
+        lib = load_library()
+        m.bind(*[ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (lib.mla_verify_tree, lib.mla_compact_kv, lib.mla_copy_pages)])
+        _helpers = m
     return _helpers
 
 
@@ -618,43 +622,20 @@ def mla_verify_tree(plan: MlaPlan, draft_tokens, target_probs, uniform, uniform_
     point masses) are [T, vocab] fp32 or bf16 with contiguous rows; ``draft_tokens`` [T]
     int32; ``uniform`` [T] and ``uniform_next`` [batch] fp32.  Returns (accept_index [T],
     num_accepted [batch], next_token [batch]), int32."""
-    N = _native()
-    T, B, dev = plan.token_capacity, plan.batch_capacity, N.device()
-    target_p, target_ld, V, code = N.probabilities(target_probs, "target_probs", dev, T)
-    draft_p, draft_ld = N.rows(draft_probs, "draft_probs", code, dev, T, V) if draft_probs is not None else (0, 0)
-    tok_p = N.tensor(draft_tokens, "draft_tokens", _I32, dev, (T,))
-    u_p = N.tensor(uniform, "uniform", _F32, dev, (T,))
-    un_p = N.tensor(uniform_next, "uniform_next", _F32, dev, (B,))
-    if accept_index is None or num_accepted is None or next_token is None:
-        made = N.empty_parts(_I32, dev, (T, B, B))  # one allocation: three took a third of the call
-        accept_index = made[0] if accept_index is None else accept_index
-        num_accepted = made[1] if num_accepted is None else num_accepted
-        next_token = made[2] if next_token is None else next_token
-    acc_p = N.tensor(accept_index, "accept_index", _I32, dev, (T,))
-    cnt_p = N.tensor(num_accepted, "num_accepted", _I32, dev, (B,))
-    nxt_p = N.tensor(next_token, "next_token", _I32, dev, (B,))
-    if stream is None:
-        stream = N.stream(dev)
-    st = load_library().mla_verify_tree(plan.handle, tok_p, target_p, target_ld, draft_p, draft_ld, V,
-                                        MLA_PROB_FP32 if code == _F32 else MLA_PROB_BF16, u_p, un_p, acc_p, cnt_p,
-                                        nxt_p, stream)
+    st, *out = _native().verify_tree(plan.handle.value, plan.token_capacity, plan.batch_capacity, draft_tokens,
+                                     target_probs, uniform, uniform_next, draft_probs, accept_index, num_accepted,
+                                     next_token, stream)
     if st != MLA_OK:
         raise MlaError(st, "mla_verify_tree")
-    return accept_index, num_accepted, next_token
+    return tuple(out)
 
 
 def mla_compact_kv(plan: MlaPlan, accept_index, num_accepted, caches, stream=None) -> None:
     """Move the accepted nodes' latent rows to consecutive cache slots in every layer's
     cache, in place (``mla_compact_kv``).  ``caches``: a list of [num_pages, page_size,
     512 + rope_dim] tensors, or one tensor with a leading layer dimension."""
-    N = _native()
-    dev = N.device()
-    ptrs = N.caches(caches, dev, plan.num_pages, plan.page_size, KV_LORA_RANK + plan.rope_dim)
-    acc_p = N.tensor(accept_index, "accept_index", _I32, dev, (plan.token_capacity,))
-    cnt_p = N.tensor(num_accepted, "num_accepted", _I32, dev, (plan.batch_capacity,))
-    if stream is None:
-        stream = N.stream(dev)
-    st = load_library().mla_compact_kv(plan.handle, acc_p, cnt_p, ptrs, len(ptrs) // 8, stream)
+    st = _native().compact_kv(plan.handle.value, plan.token_capacity, plan.batch_capacity, plan.num_pages,
+                              plan.page_size, KV_LORA_RANK + plan.rope_dim, accept_index, num_accepted, caches, stream)
     if st != MLA_OK:
         raise MlaError(st, "mla_compact_kv")
 
@@ -668,18 +649,7 @@ def mla_copy_pages(src_pages, dst_pages, caches, num_tokens=None, stream=None) -
     tok = None if num_tokens is None else _i32(num_tokens)
     if src.ndim != 1 or dst.shape != src.shape or (tok is not None and tok.shape != src.shape):
         raise MlaError(MLA_ERR_INVALID_ARGUMENT, "mla_copy_pages: table lengths")
-    N = _native()
-    dev = N.device()
-    pools = N.pools(caches, dev)
-    if pools is None:
-        return
-    ptrs, pages, page, width = pools
-    if stream is None:
-        stream = N.stream(dev)
-    dims = _Dims(128, KV_LORA_RANK, width - KV_LORA_RANK, page, pages, 1.0)
-    st = load_library().mla_copy_pages(ctypes.byref(dims), N.address(src), N.address(dst),
-                                       None if tok is None else N.address(tok), len(src), ptrs, len(ptrs) // 8,
-                                       stream)
+    st = _native().copy_pages(src, dst, tok, caches, stream)
     if st != MLA_OK:
         raise MlaError(st, "mla_copy_pages")
 

@@ -39,7 +39,7 @@ def needs_build() -> bool:
 
 def build_marshal(force: bool = False) -> str:
     """Compile the binding's native part against the installed torch (host code only)."""
-    if not force and not _older(MARSHAL, [MARSHAL_SOURCE]):
+    if not force and not _older(MARSHAL, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "mla.h")]):
         return MARSHAL
     import sysconfig
 

@@ -1,8 +1,9 @@
 // Argument marshalling of the Python binding: one native call checks a tensor and returns
 // its address.  The attribute reads behind such a check cost about 0.6 us in Python, and a
 // call over every layer's cache makes one per layer: more than the launch that follows.
-// Nothing here computes, launches or keeps anything between calls (at::empty apart, which
-// allocates an output).
+// The short calls of a speculative step are marshalled whole and made from here (a ctypes
+// call of 14 arguments costs 1 us more).  Nothing here computes, or keeps anything between
+// calls but the addresses of the library's functions.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -12,9 +13,12 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <exception>
 #include <string>
+
+#include "../../include/mla.h"
 
 namespace {
 
@@ -80,6 +84,21 @@ bool arity(Py_ssize_t n, Py_ssize_t want) {
   return false;
 }
 
+// A contiguous vector of n elements, as cuda_tensor.
+const at::Tensor* cuda_vector(PyObject* o, const char* name, int64_t type, int64_t dev, int64_t n) {
+  const at::Tensor* t = cuda_tensor(o, name, type, dev);
+  if (!t) return nullptr;
+  if (t->dim() != 1 || t->size(0) != n) {
+    value_error(std::string(name) + " must have shape " + text({n}) + ", got " + text(t->sizes()));
+    return nullptr;
+  }
+  if (!t->is_contiguous()) {
+    value_error(std::string(name) + " must be contiguous");
+    return nullptr;
+  }
+  return t;
+}
+
 // tensor(t, name, type, dev, shape) -> address of a contiguous tensor of that shape
 PyObject* py_tensor(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -107,52 +126,6 @@ PyObject* py_tensor(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (!t->is_contiguous()) return value_error(std::string(name) + " must be contiguous");
     return address_of(*t);
-  });
-}
-
-// (address, pitch) of a checked [T, V] matrix whose rows must be contiguous and apart, or
-// with the vocabulary and the type where `more`.
-PyObject* matrix(const at::Tensor& t, const char* name, int64_t T, int64_t V, int more) {
-  if (t.dim() != 2 || t.size(0) != T || t.size(1) != V)
-    return value_error(std::string(name) + " must have shape " + text({T, V}) + ", got " + text(t.sizes()));
-  if ((V > 1 && t.stride(1) != 1) || (T > 1 && t.stride(0) < V))
-    return value_error(std::string(name) + " must have contiguous rows");
-  const unsigned long long at = reinterpret_cast<uintptr_t>(t.data_ptr());
-  const long long pitch = T > 1 ? t.stride(0) : V;
-  if (more >= 0) return Py_BuildValue("(KLLi)", at, pitch, static_cast<long long>(V), more);
-  return Py_BuildValue("(KL)", at, pitch);
-}
-
-// rows(t, name, type, dev, tokens, vocab) -> (address, pitch)
-PyObject* py_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    if (!arity(n, 6)) return nullptr;
-    const char* name = PyUnicode_AsUTF8(a[1]);
-    int64_t type, dev, T, V;
-    if (!name || !integer(a[2], &type) || !integer(a[3], &dev) || !integer(a[4], &T) || !integer(a[5], &V))
-      return nullptr;
-    const at::Tensor* t = cuda_tensor(a[0], name, type, dev);
-    return t ? matrix(*t, name, T, V, -1) : nullptr;
-  });
-}
-
-// probabilities(t, name, dev, tokens) -> (address, pitch, vocab, type) of a float32 or
-// bfloat16 matrix
-PyObject* py_probabilities(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    if (!arity(n, 4)) return nullptr;
-    const char* name = PyUnicode_AsUTF8(a[1]);
-    int64_t dev, T;
-    if (!name || !integer(a[2], &dev) || !integer(a[3], &T)) return nullptr;
-    int type = -1;
-    if (THPVariable_Check(a[0])) {
-      const at::Tensor& t = THPVariable_Unpack(a[0]);
-      if (t.dim() == 2 && t.size(1) > 0)
-        type = t.scalar_type() == at::kBFloat16 ? 0 : t.scalar_type() == at::kFloat ? 1 : -1;
-    }
-    if (type < 0) return value_error(std::string(name) + " must be a [T, vocab] tensor of float32 or bfloat16");
-    const at::Tensor* t = cuda_tensor(a[0], name, type, dev);
-    return t ? matrix(*t, name, T, t->size(1), type) : nullptr;
   });
 }
 
@@ -223,52 +196,6 @@ PyObject* cache_addresses(PyObject* o, const CacheShape& want) {
   return out;
 }
 
-// caches(c, dev, pages, page, width) -> bytes of the layers' addresses
-PyObject* py_caches(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    CacheShape want;
-    if (!arity(n, 5) || !want.parse(a + 1)) return nullptr;
-    return cache_addresses(a[0], want);
-  });
-}
-
-// pools(c, dev) -> (bytes of the layers' addresses, pages, page, width), by the first
-// cache's shape; None where there is no cache
-PyObject* py_pools(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    CacheShape want;
-    if (!arity(n, 2) || !integer(a[1], &want.dev)) return nullptr;
-    THPObjectPtr held;
-    PyObject* first = a[0];
-    if (!THPVariable_Check(first)) {
-      const Py_ssize_t layers = PySequence_Size(a[0]);
-      if (layers < 0) return nullptr;
-      if (layers == 0) Py_RETURN_NONE;
-      held = PySequence_GetItem(a[0], 0);
-      first = held.get();
-      if (!first) return nullptr;
-    }
-    int64_t dims = 0;
-    if (THPVariable_Check(first)) {
-      const at::Tensor& t = THPVariable_Unpack(first);
-      dims = t.dim();
-      if (dims == 3 || (dims == 4 && first == a[0])) {
-        if (dims == 4 && t.size(0) == 0) Py_RETURN_NONE;
-        want.pages = t.size(dims - 3);
-        want.page = t.size(dims - 2);
-        want.width = t.size(dims - 1);
-      } else {
-        dims = 0;
-      }
-    }
-    if (dims == 0) return value_error("caches must be [num_pages, page_size, 512 + rope_dim]");
-    PyObject* at = cache_addresses(a[0], want);
-    if (!at) return nullptr;
-    return Py_BuildValue("(NLLL)", at, static_cast<long long>(want.pages), static_cast<long long>(want.page),
-                         static_cast<long long>(want.width));
-  });
-}
-
 // empty(type, dev, shape) -> a new tensor
 PyObject* py_empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -284,38 +211,15 @@ PyObject* py_empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// empty_parts(type, dev, sizes) -> new one-dimensional tensors, parts of one allocation
-PyObject* py_empty_parts(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    if (!arity(n, 3)) return nullptr;
-    int64_t type, dev, sum = 0, size[8];
-    const Py_ssize_t parts = PyTuple_Size(a[2]);
-    if (!integer(a[0], &type) || !integer(a[1], &dev) || parts < 0) return nullptr;
-    if (parts > 8) return value_error("at most eight parts");
-    for (Py_ssize_t i = 0; i < parts; ++i) {
-      if (!integer(PyTuple_GET_ITEM(a[2], i), &size[i])) return nullptr;
-      sum += size[i];
-    }
-    const at::Tensor all = at::empty({sum}, at::TensorOptions().dtype(kTypes[type]).device(at::kCUDA, dev));
-    PyObject* out = PyTuple_New(parts);
-    int64_t from = 0;
-    for (Py_ssize_t i = 0; out && i < parts; from += size[i++]) {
-      auto impl = all.unsafeGetTensorImpl()->shallow_copy_and_detach(c10::VariableVersion(0), true);
-      impl->set_storage_offset(from);
-      impl->set_sizes_contiguous({size[i]});
-      PyObject* t = THPVariable_Wrap(at::Tensor(std::move(impl)));
-      if (t)
-        PyTuple_SET_ITEM(out, i, t);
-      else
-        Py_CLEAR(out);
-    }
-    return out;
-  });
+int64_t current_device() { return c10::cuda::device_count() > 0 ? c10::cuda::current_device() : -1; }
+
+void* current_stream(int64_t dev) {
+  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
 }
 
 // device() -> the current CUDA device, -1 on a machine without one
 PyObject* py_device(PyObject*, PyObject*) {
-  return guarded([] { return PyLong_FromLong(c10::cuda::device_count() > 0 ? c10::cuda::current_device() : -1); });
+  return guarded([] { return PyLong_FromLongLong(current_device()); });
 }
 
 // stream(dev) -> handle of torch's current stream of the device
@@ -323,8 +227,7 @@ PyObject* py_stream(PyObject*, PyObject* o) {
   return guarded([&]() -> PyObject* {
     int64_t dev;
     if (!integer(o, &dev)) return nullptr;
-    return PyLong_FromUnsignedLongLong(
-        reinterpret_cast<uintptr_t>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream()));
+    return PyLong_FromUnsignedLongLong(reinterpret_cast<uintptr_t>(current_stream(dev)));
   });
 }
 
@@ -337,15 +240,219 @@ PyObject* py_address(PyObject*, PyObject* o) {
   return r;
 }
 
+// ------------------------------------------------------------------ whole calls
+// The library's functions, as the binding loaded it.
+decltype(&mla_verify_tree) g_verify = nullptr;
+decltype(&mla_compact_kv) g_compact = nullptr;
+decltype(&mla_copy_pages) g_copy = nullptr;
+
+// bind(verify_tree, compact_kv, copy_pages): their addresses
+PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  int64_t at[3];
+  if (!arity(n, 3) || !integer(a[0], &at[0]) || !integer(a[1], &at[1]) || !integer(a[2], &at[2])) return nullptr;
+  g_verify = reinterpret_cast<decltype(g_verify)>(at[0]);
+  g_compact = reinterpret_cast<decltype(g_compact)>(at[1]);
+  g_copy = reinterpret_cast<decltype(g_copy)>(at[2]);
+  Py_RETURN_NONE;
+}
+
+// A stream argument: its handle, or None for the device's current stream.
+bool stream_of(PyObject* o, int64_t dev, void** s) {
+  if (o == Py_None) {
+    *s = current_stream(dev);
+    return true;
+  }
+  int64_t v;
+  if (!integer(o, &v)) return false;
+  *s = reinterpret_cast<void*>(v);
+  return true;
+}
+
+mla_plan_t plan_of(int64_t handle) { return reinterpret_cast<mla_plan_t>(handle); }
+
+// A [T, vocab] matrix of float32 or bfloat16 whose rows are contiguous and apart; `type`
+// and `vocab` receive the first one's and bind the next (type < 0, vocab < 0: not known).
+const at::Tensor* probabilities(PyObject* o, const char* name, int64_t dev, int64_t T, int64_t* type, int64_t* vocab,
+                                int64_t* pitch) {
+  if (*type < 0) {
+    if (THPVariable_Check(o)) {
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (t.dim() == 2 && t.size(1) > 0) {
+        *type = t.scalar_type() == at::kBFloat16 ? 0 : t.scalar_type() == at::kFloat ? 1 : -1;
+        *vocab = t.size(1);
+      }
+    }
+    if (*type < 0) {
+      value_error(std::string(name) + " must be a [T, vocab] tensor of float32 or bfloat16");
+      return nullptr;
+    }
+  }
+  const at::Tensor* t = cuda_tensor(o, name, *type, dev);
+  if (!t) return nullptr;
+  if (t->dim() != 2 || t->size(0) != T || t->size(1) != *vocab) {
+    value_error(std::string(name) + " must have shape " + text({T, *vocab}) + ", got " + text(t->sizes()));
+    return nullptr;
+  }
+  if ((*vocab > 1 && t->stride(1) != 1) || (T > 1 && t->stride(0) < *vocab)) {
+    value_error(std::string(name) + " must have contiguous rows");
+    return nullptr;
+  }
+  *pitch = T > 1 ? t->stride(0) : *vocab;
+  return t;
+}
+
+// verify_tree(plan, T, B, draft_tokens, target, uniform, uniform_next, draft, accept_index,
+// num_accepted, next_token, stream) -> (status, accept_index, num_accepted, next_token).
+// Outputs that are None are made, as parts of one allocation (three took a third of the
+// call).
+PyObject* py_verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    int64_t plan, T, B;
+    if (!arity(n, 12) || !integer(a[0], &plan) || !integer(a[1], &T) || !integer(a[2], &B)) return nullptr;
+    const int64_t dev = current_device();
+    int64_t type = -1, vocab = -1, ld_target = 0, ld_draft = 0;
+    const at::Tensor* target = probabilities(a[4], "target_probs", dev, T, &type, &vocab, &ld_target);
+    const at::Tensor* draft = nullptr;
+    if (!target) return nullptr;
+    if (a[7] != Py_None && !(draft = probabilities(a[7], "draft_probs", dev, T, &type, &vocab, &ld_draft)))
+      return nullptr;
+    const at::Tensor* tokens = cuda_vector(a[3], "draft_tokens", 2, dev, T);
+    const at::Tensor* uniform = tokens ? cuda_vector(a[5], "uniform", 1, dev, T) : nullptr;
+    const at::Tensor* next = uniform ? cuda_vector(a[6], "uniform_next", 1, dev, B) : nullptr;
+    if (!next) return nullptr;
+    static const char* const kNames[] = {"accept_index", "num_accepted", "next_token"};
+    const int64_t size[] = {T, B, B}, from[] = {0, T, T + B};
+    at::Tensor made, out[3];
+    for (int i = 0; i < 3; ++i) {
+      if (a[8 + i] != Py_None) {
+        const at::Tensor* t = cuda_vector(a[8 + i], kNames[i], 2, dev, size[i]);
+        if (!t) return nullptr;
+        out[i] = *t;
+        continue;
+      }
+      if (!made.defined()) made = at::empty({T + 2 * B}, at::TensorOptions().dtype(at::kInt).device(at::kCUDA, dev));
+      auto impl = made.unsafeGetTensorImpl()->shallow_copy_and_detach(c10::VariableVersion(0), true);
+      impl->set_storage_offset(from[i]);
+      impl->set_sizes_contiguous({size[i]});
+      out[i] = at::Tensor(std::move(impl));
+    }
+    void* stream;
+    if (!stream_of(a[11], dev, &stream)) return nullptr;
+    mla_status st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = g_verify(plan_of(plan), static_cast<const int32_t*>(tokens->data_ptr()), target->data_ptr(), ld_target,
+                  draft ? draft->data_ptr() : nullptr, ld_draft, static_cast<int32_t>(std::min<int64_t>(vocab, INT32_MAX)),
+                  type == 0 ? MLA_PROB_BF16 : MLA_PROB_FP32, static_cast<const float*>(uniform->data_ptr()),
+                  static_cast<const float*>(next->data_ptr()), static_cast<int32_t*>(out[0].data_ptr()),
+                  static_cast<int32_t*>(out[1].data_ptr()), static_cast<int32_t*>(out[2].data_ptr()), stream);
+    Py_END_ALLOW_THREADS;
+    PyObject* r = PyTuple_New(4);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, PyLong_FromLong(st));
+    for (int i = 0; i < 3; ++i) {
+      PyObject* t = a[8 + i];
+      if (t == Py_None)
+        t = THPVariable_Wrap(out[i]);
+      else
+        Py_INCREF(t);
+      PyTuple_SET_ITEM(r, 1 + i, t);
+    }
+    return r;
+  });
+}
+
+// compact_kv(plan, T, B, pages, page, width, accept_index, num_accepted, caches, stream) ->
+// status
+PyObject* py_compact_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    int64_t plan, T, B;
+    CacheShape want;
+    if (!arity(n, 10) || !integer(a[0], &plan) || !integer(a[1], &T) || !integer(a[2], &B) ||
+        !integer(a[3], &want.pages) || !integer(a[4], &want.page) || !integer(a[5], &want.width))
+      return nullptr;
+    want.dev = current_device();
+    THPObjectPtr caches(cache_addresses(a[8], want));
+    if (!caches) return nullptr;
+    const at::Tensor* acc = cuda_vector(a[6], "accept_index", 2, want.dev, T);
+    const at::Tensor* cnt = acc ? cuda_vector(a[7], "num_accepted", 2, want.dev, B) : nullptr;
+    void* stream;
+    if (!cnt || !stream_of(a[9], want.dev, &stream)) return nullptr;
+    mla_status st;
+    void* const* list = reinterpret_cast<void* const*>(PyBytes_AS_STRING(caches.get()));
+    const int32_t layers = static_cast<int32_t>(PyBytes_GET_SIZE(caches.get()) / 8);
+    Py_BEGIN_ALLOW_THREADS;
+    st = g_compact(plan_of(plan), static_cast<const int32_t*>(acc->data_ptr()),
+                   static_cast<const int32_t*>(cnt->data_ptr()), list, layers, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// A C-contiguous buffer of n int32, held until the object goes.
+struct Table {
+  Py_buffer b{};
+  bool open(PyObject* o) { return PyObject_GetBuffer(o, &b, PyBUF_C_CONTIGUOUS) == 0; }
+  const int32_t* data() const { return static_cast<const int32_t*>(b.buf); }
+  ~Table() {
+    if (b.obj) PyBuffer_Release(&b);
+  }
+};
+
+// copy_pages(src, dst, tokens, caches, stream) -> status.  The tables are int32 arrays of
+// one length (tokens may be None); the geometry is the first cache's.
+PyObject* py_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Table src, dst, tokens;
+    if (!arity(n, 5) || !src.open(a[0]) || !dst.open(a[1]) || (a[2] != Py_None && !tokens.open(a[2]))) return nullptr;
+    const Py_ssize_t pairs = src.b.len / 4;
+    if (dst.b.len != src.b.len || (tokens.b.obj && tokens.b.len != src.b.len) || pairs > INT32_MAX)
+      return value_error("tables of different lengths");
+    CacheShape want;
+    want.dev = current_device();
+    THPObjectPtr held;
+    PyObject* first = a[3];
+    if (!THPVariable_Check(first)) {
+      const Py_ssize_t layers = PySequence_Size(a[3]);
+      if (layers < 0) return nullptr;
+      if (layers == 0) return PyLong_FromLong(MLA_OK);
+      held = PySequence_GetItem(a[3], 0);
+      first = held.get();
+      if (!first) return nullptr;
+    }
+    int64_t dims = 0;
+    if (THPVariable_Check(first)) {
+      const at::Tensor& t = THPVariable_Unpack(first);
+      if (t.dim() == 3 || (t.dim() == 4 && first == a[3])) {
+        dims = t.dim();
+        want.pages = t.size(dims - 3);
+        want.page = t.size(dims - 2);
+        want.width = t.size(dims - 1);
+      }
+    }
+    if (dims == 0) return value_error("caches must be [num_pages, page_size, 512 + rope_dim]");
+    THPObjectPtr caches(cache_addresses(a[3], want));
+    void* stream;
+    if (!caches || !stream_of(a[4], want.dev, &stream)) return nullptr;
+    auto i32 = [](int64_t v) { return static_cast<int32_t>(std::min<int64_t>(v, INT32_MAX)); };
+    const mla_dims d = {128, 512, i32(want.width - 512), i32(want.page), i32(want.pages), 1.f};
+    mla_status st;
+    void* const* list = reinterpret_cast<void* const*>(PyBytes_AS_STRING(caches.get()));
+    const int32_t layers = static_cast<int32_t>(PyBytes_GET_SIZE(caches.get()) / 8);
+    Py_BEGIN_ALLOW_THREADS;
+    st = g_copy(&d, src.data(), dst.data(), tokens.b.obj ? tokens.data() : nullptr, static_cast<int32_t>(pairs), list,
+                layers, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
 PyMethodDef kMethods[] = {
     {"tensor", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_tensor)), METH_FASTCALL, nullptr},
-    {"rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_rows)), METH_FASTCALL, nullptr},
     {"cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_cache)), METH_FASTCALL, nullptr},
-    {"caches", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_caches)), METH_FASTCALL, nullptr},
-    {"pools", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_pools)), METH_FASTCALL, nullptr},
-    {"probabilities", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_probabilities)), METH_FASTCALL,
-     nullptr},
-    {"empty_parts", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_empty_parts)), METH_FASTCALL, nullptr},
+    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_bind)), METH_FASTCALL, nullptr},
+    {"verify_tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_verify_tree)), METH_FASTCALL, nullptr},
+    {"compact_kv", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_compact_kv)), METH_FASTCALL, nullptr},
+    {"copy_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_copy_pages)), METH_FASTCALL, nullptr},
     {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_empty)), METH_FASTCALL, nullptr},
     {"device", py_device, METH_NOARGS, nullptr},
     {"stream", py_stream, METH_O, nullptr},
