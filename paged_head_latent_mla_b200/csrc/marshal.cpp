@@ -256,6 +256,12 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+bool bound() {
+  if (g_verify && g_compact && g_copy) return true;
+  PyErr_SetString(PyExc_RuntimeError, "the library's functions are not bound");
+  return false;
+}
+
 // A stream argument: its handle, or None for the device's current stream.
 bool stream_of(PyObject* o, int64_t dev, void** s) {
   if (o == Py_None) {
@@ -308,7 +314,7 @@ const at::Tensor* probabilities(PyObject* o, const char* name, int64_t dev, int6
 PyObject* py_verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     int64_t plan, T, B;
-    if (!arity(n, 12) || !integer(a[0], &plan) || !integer(a[1], &T) || !integer(a[2], &B)) return nullptr;
+    if (!bound() || !arity(n, 12) || !integer(a[0], &plan) || !integer(a[1], &T) || !integer(a[2], &B)) return nullptr;
     const int64_t dev = current_device();
     int64_t type = -1, vocab = -1, ld_target = 0, ld_draft = 0;
     const at::Tensor* target = probabilities(a[4], "target_probs", dev, T, &type, &vocab, &ld_target);
@@ -346,18 +352,12 @@ PyObject* py_verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   static_cast<const float*>(next->data_ptr()), static_cast<int32_t*>(out[0].data_ptr()),
                   static_cast<int32_t*>(out[1].data_ptr()), static_cast<int32_t*>(out[2].data_ptr()), stream);
     Py_END_ALLOW_THREADS;
-    PyObject* r = PyTuple_New(4);
-    if (!r) return nullptr;
-    PyTuple_SET_ITEM(r, 0, PyLong_FromLong(st));
+    THPObjectPtr items[3];
     for (int i = 0; i < 3; ++i) {
-      PyObject* t = a[8 + i];
-      if (t == Py_None)
-        t = THPVariable_Wrap(out[i]);
-      else
-        Py_INCREF(t);
-      PyTuple_SET_ITEM(r, 1 + i, t);
+      items[i] = a[8 + i] == Py_None ? THPVariable_Wrap(out[i]) : Py_NewRef(a[8 + i]);
+      if (!items[i]) return nullptr;
     }
-    return r;
+    return Py_BuildValue("(iNNN)", static_cast<int>(st), items[0].release(), items[1].release(), items[2].release());
   });
 }
 
@@ -367,7 +367,7 @@ PyObject* py_compact_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     int64_t plan, T, B;
     CacheShape want;
-    if (!arity(n, 10) || !integer(a[0], &plan) || !integer(a[1], &T) || !integer(a[2], &B) ||
+    if (!bound() || !arity(n, 10) || !integer(a[0], &plan) || !integer(a[1], &T) || !integer(a[2], &B) ||
         !integer(a[3], &want.pages) || !integer(a[4], &want.page) || !integer(a[5], &want.width))
       return nullptr;
     want.dev = current_device();
@@ -403,7 +403,8 @@ struct Table {
 PyObject* py_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     Table src, dst, tokens;
-    if (!arity(n, 5) || !src.open(a[0]) || !dst.open(a[1]) || (a[2] != Py_None && !tokens.open(a[2]))) return nullptr;
+    if (!bound() || !arity(n, 5) || !src.open(a[0]) || !dst.open(a[1]) || (a[2] != Py_None && !tokens.open(a[2])))
+      return nullptr;
     const Py_ssize_t pairs = src.b.len / 4;
     if (dst.b.len != src.b.len || (tokens.b.obj && tokens.b.len != src.b.len) || pairs > INT32_MAX)
       return value_error("tables of different lengths");

@@ -255,3 +255,25 @@ def test_python_checks():
     with pytest.raises(M.MlaError):
         M.mla_copy_pages([0], [1, 2], [torch.zeros(9, 16, 576, dtype=torch.bfloat16)])
     M.mla_copy_pages([], [], [])
+
+
+def test_python_checks_survive_odd_arguments():
+    """Arguments of other kinds raise; a destroyed plan does; nothing is called."""
+    import torch
+
+    plan, _ = plan_tree([2], [50], [-1, 0])
+    for bad in (None, 3, "x", [1], torch.zeros(2, 0), torch.zeros(2, 8, dtype=torch.float16)):
+        with pytest.raises(ValueError):
+            M.mla_verify_tree(plan, bad, bad, bad, bad)
+    for caches in (None, 5):
+        with pytest.raises(TypeError):
+            M.mla_compact_kv(plan, torch.zeros(2), torch.zeros(1), caches)
+        with pytest.raises(TypeError):
+            M.mla_copy_pages([0], [1], caches)
+    with pytest.raises(ValueError):
+        M.mla_copy_pages([0], [1], [object()])
+    with pytest.raises(ValueError):
+        M.mla_compact_kv(plan, torch.zeros(2), torch.zeros(1), [object()])
+    plan.destroy()
+    with pytest.raises(RuntimeError):
+        M.mla_compact_kv(plan, torch.zeros(2), torch.zeros(1), [])
