@@ -26,8 +26,12 @@
  *
  * Threading and streams: a plan belongs to the CUDA device that was current when it
  * was made; call mla_run with that device current.  Calls on one plan must not
- * overlap on the host.  Every function returns a status code; nothing throws,
- * traps or aborts.
+ * overlap on the host.  On the GPU, runs of one plan and updates of it must be ordered
+ * among streams by the caller (they share its workspace and lists); calls that only read
+ * the plan (mla_append_kv, mla_verify_tree, mla_compact_kv) may run side by side on
+ * several streams, as far as their own buffers allow.  mla_plan_check, mla_plan_destroy
+ * and an update that grows a buffer wait for the plan's last call on every stream.
+ * Every function returns a status code; nothing throws, traps or aborts.
  */
 #ifndef PAGED_MLA_B200_H
 #define PAGED_MLA_B200_H
@@ -178,7 +182,7 @@ mla_status mla_plan(const mla_dims* dims, int32_t batch, const int32_t* qo_indpt
 mla_status mla_run(mla_plan_t plan, const void* q_nope, const void* q_pe, const void* cache,
                    void* out, float* lse, void* stream);
 
-/* Wait for the plan's last run to finish and report (then clear) its device status
+/* Wait for the plan's last calls to finish and report (then clear) its device status
  * word: MLA_OK, or MLA_ERR_DEVICE_TIMEOUT when an in-kernel wait gave up.  The kernel
  * that records the first error also writes it to a host-mapped copy, which this call
  * reads: no device-to-host copy, so it waits for the plan's launches only, not for
@@ -219,11 +223,11 @@ mla_status mla_plan_describe(mla_plan_t plan, int32_t* kv_len, int32_t* work, in
  * A graph plan keeps every device address and launch shape: a CUDA graph that captured
  * mla_run (or mla_append_kv) on it replays the new step.  The step must fit the bucket
  * (batch, tokens and page ids within the graph bounds), else INVALID_ARGUMENT and the
- * plan is unchanged.  Other plans may grow their buffers (waiting for their last run
- * first when they do).  The host staging is double-buffered: the call waits only for
- * the upload of two updates ago, so the host may run one step ahead of the GPU
- * (FlashInferMLAManager.force_double_buffer describes the race this avoids).  It must
- * not be called while `stream` is being captured into a graph (the upload belongs to
+ * plan is unchanged.  Other plans may grow their buffers (waiting for their last call
+ * on every stream first when they do).  The host staging is double-buffered: the call
+ * waits only for the upload of two updates ago, so the host may run one step ahead of
+ * the GPU (FlashInferMLAManager.force_double_buffer describes the race this avoids).  It
+ * must not be called while `stream` is being captured into a graph (the upload belongs to
  * the moment of re-planning, not to every replay): INVALID_ARGUMENT.
  * Errors: INVALID_ARGUMENT, OUT_OF_MEMORY, CUDA; on error the plan still describes and
  * runs its previous step. */
@@ -442,7 +446,8 @@ mla_status mla_copy_pages(const mla_dims* dims, const int32_t* src_pages, const 
                           const int32_t* num_tokens, int32_t num_pairs, void* const* caches, int32_t num_caches,
                           void* stream);
 
-/* Wait for the plan's last run, then free everything it owns.  NULL is a no-op. */
+/* Wait for the plan's last call on every stream, then free everything it owns.  NULL is a
+ * no-op. */
 void mla_plan_destroy(mla_plan_t plan);
 
 /* Static string for a status code. */

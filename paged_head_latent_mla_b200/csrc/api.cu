@@ -55,7 +55,14 @@ struct mla_plan_s {
   bool upload_pending[2] = {false, false};
   int64_t uploads = 0;
   size_t blob_cap = 0, ws_cap = 0;  // capacities of the pooled device buffers
-  cudaEvent_t ev_last = nullptr;
+  // The last use of the plan's buffers on each stream that used them (see note_use).
+  struct StreamUse {
+    unsigned long long stream;  // cudaStreamGetId: never that of an earlier stream
+    cudaEvent_t ev;
+  };
+  static constexpr int kStreams = 8;
+  StreamUse uses[kStreams] = {};
+  int num_uses = 0, next_fold = 0;
   int32_t* h_status = nullptr;  // host-mapped mirror of the status word (see status_slot_take)
   // kernel timing ring (MLA_DEBUG_KERNEL_TIMING): 3 events per run
   static constexpr int kRing = 256;
@@ -242,14 +249,48 @@ void status_slot_give(int32_t* slot) {
   g_status_free->push_back(slot);
 }
 
+// Record that the work enqueued on `s` so far uses the plan's buffers.  Every stream has an
+// event of its own: launches that only read a plan (mla_verify_tree, mla_compact_kv,
+// mla_append_kv) may run side by side, and one event, recorded by the last of them alone,
+// would hide the others.  Beyond kStreams streams two share an event, the later one's next
+// work waiting for the earlier one's last use (nothing is queried or waited for here).
+cudaError_t note_use(mla_plan_s* p, cudaStream_t s) {
+  unsigned long long id = 0;
+  cudaError_t e = cudaStreamGetId(s, &id);
+  if (e != cudaSuccess) return e;
+  int i = 0;
+  while (i < p->num_uses && p->uses[i].stream != id) ++i;
+  if (i == p->num_uses) {
+    const cudaEvent_t ev = i < mla_plan_s::kStreams ? event_take(p->device) : nullptr;
+    if (ev) {
+      p->uses[p->num_uses++] = {id, ev};
+    } else {
+      if (p->num_uses == 0) return cudaErrorMemoryAllocation;
+      i = p->next_fold++ % p->num_uses;
+      if ((e = cudaStreamWaitEvent(s, p->uses[i].ev, 0)) != cudaSuccess) return e;
+      p->uses[i].stream = id;
+    }
+  }
+  return cudaEventRecord(p->uses[i].ev, s);
+}
+
+cudaError_t wait_uses(const mla_plan_s* p) {
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < p->num_uses; ++i) {
+    const cudaError_t one = cudaEventSynchronize(p->uses[i].ev);
+    if (one != cudaSuccess) e = one;
+  }
+  return e;
+}
+
 // Wait until no launch or upload of the plan can still be reading its buffers.
 void quiesce(mla_plan_s* p) {
   if (p->captured) {
     // graphs captured from the plan may have replayed on any stream
     cudaDeviceSynchronize();
     cudaGetLastError();
-  } else if (p->ev_last) {
-    cudaEventSynchronize(p->ev_last);
+  } else {
+    wait_uses(p);
   }
   for (int i = 0; i < 2; ++i)
     if (p->ev_upload[i] && p->upload_pending[i]) cudaEventSynchronize(p->ev_upload[i]);
@@ -259,7 +300,7 @@ void free_plan(mla_plan_s* p) {
   if (!p) return;
   if (!p->host_only) {
     quiesce(p);
-    event_give(p->device, p->ev_last);
+    for (int i = 0; i < p->num_uses; ++i) event_give(p->device, p->uses[i].ev);
     for (int i = 0; i < 2; ++i) event_give(p->device, p->ev_upload[i]);
     if (p->ring) {
       for (int i = 0; i < 3 * mla_plan_s::kRing; ++i)
@@ -553,8 +594,7 @@ mla_status enqueue_attention(mla_plan_t p, AttnLaunch& a, cudaStream_t s) {
     if (cudaEventRecord(ev[2], s) != cudaSuccess) return MLA_ERR_CUDA;
     ++p->runs;
   }
-  if (!capturing && cudaEventRecord(p->ev_last, s) != cudaSuccess) return MLA_ERR_CUDA;
-  return MLA_OK;
+  return capturing || note_use(p, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 // Bookkeeping after a launch that reads the plan's device lists.
@@ -563,7 +603,7 @@ mla_status note_launch(mla_plan_t p, cudaStream_t s) {
     p->captured = true;
     return MLA_OK;
   }
-  return cudaEventRecord(p->ev_last, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return note_use(p, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 // No C++ exception leaves a C entry: host memory is all that can run out.
@@ -671,9 +711,9 @@ mla_status plan_create(bool tree, const mla_dims* dims, int32_t batch, const int
     for (int i = 0; i < 3 * mla_plan_s::kRing; ++i)
       if (cudaEventCreate(&p->ring[i]) != cudaSuccess) { cudaGetLastError(); return MLA_ERR_CUDA; }
   }
-  if (!(p->ev_last = event_take(p->device)) || !(p->h_status = status_slot_take())) return MLA_ERR_CUDA;
+  if (!(p->h_status = status_slot_take())) return MLA_ERR_CUDA;
   st = upload(p, kv_indices, n_idx, s);
-  if (st != MLA_OK || cudaEventRecord(p->ev_last, s) != cudaSuccess) {
+  if (st != MLA_OK || note_use(p, s) != cudaSuccess) {
     cudaGetLastError();
     return st != MLA_OK ? st : MLA_ERR_CUDA;
   }
@@ -723,8 +763,7 @@ mla_status plan_update(bool tree, mla_plan_t p, int32_t batch, const int32_t* qo
     return st;
   }
   remember_tables(p, batch, qo_indptr, kv_indptr, kv_indices, last_page_len, parents);
-  if (cudaEventRecord(p->ev_last, s) != cudaSuccess) return MLA_ERR_CUDA;
-  return MLA_OK;
+  return note_use(p, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace
@@ -917,7 +956,9 @@ mla_status mla_append_kv(mla_plan_t p, const void* kv_new, void* cache, void* st
   mla_status st = append_launch_of(p, kv_new, cache, &ap, &n);
   if (st != MLA_OK) return st;
   if (n == 0) return MLA_OK;
-  return launch_append(ap, n, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (launch_append(ap, n, s) != cudaSuccess) return MLA_ERR_CUDA;
+  return note_launch(p, s);
 }
 
 mla_status mla_run_append(mla_plan_t p, const void* q_nope, const void* q_pe, const void* kv_new, void* cache,
@@ -939,7 +980,7 @@ mla_status mla_run_append(mla_plan_t p, const void* q_nope, const void* q_pe, co
     if (launch_append(app, n, s) != cudaSuccess) return MLA_ERR_CUDA;
     a.wait_prior_grid = true;  // only the key loads wait for the append's writes
   }
-  if (!attend) return MLA_OK;
+  if (!attend) return note_launch(p, s);
   return enqueue_attention(p, a, s);
 }
 
@@ -961,7 +1002,7 @@ mla_status mla_plan_check(mla_plan_t p) {
   if (p->host_only) return MLA_OK;
   if (p->captured) {
     if (cudaDeviceSynchronize() != cudaSuccess) return MLA_ERR_CUDA;
-  } else if (cudaEventSynchronize(p->ev_last) != cudaSuccess) {
+  } else if (wait_uses(p) != cudaSuccess) {
     return MLA_ERR_CUDA;
   }
   // the launches have finished: the mirror holds the first error they recorded

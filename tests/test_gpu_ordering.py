@@ -77,3 +77,119 @@ def test_what_follows_a_graph_plan_waits_for_its_attention(tree, captured):
     assert M.mla_plan_check(plan) == M.MLA_OK
     del g
     plan.destroy()
+
+
+# ------------------------------------------------------------------ several streams, one plan
+CALLS = ["append", "run_append", "verify", "compact"]
+
+
+class Step:
+    """A tree plan over eight rows, and calls on it that two streams may make side by side
+    (each has outputs of its own; a compaction of the path (0,) moves nothing)."""
+
+    def __init__(self, **kw):
+        self.d = d = make_custom([4] * 8, [100] * 8, 16, 16, seed=52)
+        self.plan = plan_of(d, True, **kw)
+        self.q = d.q_nope.to(DEV), d.q_pe.to(DEV)
+        self.cache = d.cache.to(DEV)
+        self.kv = torch.zeros((32, 576), dtype=torch.bfloat16, device=DEV)
+        self.probs = torch.full((32, 64), 1 / 64, device=DEV)
+        self.tok = torch.zeros(32, dtype=torch.int32, device=DEV)
+        self.u = torch.zeros(32, device=DEV)
+        self.acc = torch.full((32,), -1, dtype=torch.int32, device=DEV)
+        self.cnt = torch.zeros(8, dtype=torch.int32, device=DEV)
+        torch.cuda.synchronize()
+
+    def call(self, what, plan=None):
+        plan = plan or self.plan
+        if what == "append":
+            M.mla_append_kv(plan, self.kv, self.cache)
+        elif what == "run_append":
+            M.mla_run(plan, *self.q, self.cache, kv_new=self.kv)
+        elif what == "verify":
+            M.mla_verify_tree(plan, self.tok, self.probs, self.u, self.u[:8])
+        else:
+            M.mla_compact_kv(plan, self.acc, self.cnt, [self.cache])
+
+
+@pytest.fixture(scope="module")
+def loaded(lib):
+    """Every kernel has run once: a kernel's first launch loads it, which may wait for the
+    device."""
+    step = Step()
+    for what in CALLS:
+        step.call(what)
+    assert M.mla_plan_check(step.plan) == M.MLA_OK
+
+
+def delayed(stream, f):
+    """Enqueue f on the stream behind 50 ms or so of other work; the event after it."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(100_000_000)
+        f()
+        return stream.record_event()
+
+
+@pytest.mark.parametrize("after", ["destroy", "check", "grow"])
+@pytest.mark.parametrize("first", CALLS)
+def test_a_plan_waits_for_its_calls_on_every_stream(first, after, loaded):
+    """The buffers of a plan that is destroyed go to the next one: not before the last call
+    on each stream is done."""
+    step = Step()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    done = delayed(a, lambda: step.call(first))
+    with torch.cuda.stream(b):
+        step.call("verify")
+    assert not done.query()
+    if after == "destroy":
+        step.plan.destroy()
+    elif after == "check":
+        assert M.mla_plan_check(step.plan) == M.MLA_OK
+    else:
+        rows = np.arange(4001, dtype=np.int32)  # of one page each, the same page
+        M.mla_plan_tree_update(step.plan, 4 * rows, rows, 0 * rows[1:], 4 + 0 * rows[1:],
+                               np.tile(np.arange(-1, 3, dtype=np.int32), 4000), stream=b.cuda_stream)
+    assert done.query()
+    torch.cuda.synchronize()
+
+
+def test_a_plan_waits_for_many_streams(loaded):
+    """More streams than a plan keeps events for."""
+    step = Step()
+    streams = [torch.cuda.Stream() for _ in range(20)]
+    done = [delayed(s, lambda: step.call("compact")) for s in streams[:3]]
+    for s in streams[3:]:
+        with torch.cuda.stream(s):
+            step.call("verify")
+            done.append(s.record_event())
+    assert not done[0].query()
+    step.plan.destroy()
+    assert all(e.query() for e in done)
+    torch.cuda.synchronize()
+
+
+def test_calls_on_two_streams_do_not_wait_for_one_another(loaded):
+    step = Step()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    late = delayed(a, lambda: step.call("compact"))
+    with torch.cuda.stream(b):
+        for what in ("verify", "compact", "verify"):
+            step.call(what)
+        b.synchronize()
+    assert not late.query()
+    torch.cuda.synchronize()
+
+
+def test_a_captured_append_is_waited_for(loaded):
+    """A graph that captured only an append may replay on any stream."""
+    step = Step(graph_max_batch=8, graph_max_tokens=32, graph_max_page_ids=56)
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        step.call("append")
+    done = delayed(s, g.replay)
+    assert not done.query()
+    step.plan.destroy()
+    assert done.query()
+    torch.cuda.synchronize()
+    del g
