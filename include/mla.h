@@ -340,8 +340,10 @@ mla_status mla_run_noalloc(const mla_dims* dims, int32_t batch, const int32_t* q
  * Every row needs k_b >= q_b (its nodes have cache slots), and a row that is not a chain
  * at most MLA_TREE_MAX_NODES nodes.  Graph buckets, split keys and the cascade apply (a
  * shared prefix then ends with the rows' context); context_only is refused.  mla_run,
- * mla_append_kv and mla_run_append take the plan as any other.  Where a masked node's
- * latent row holds an infinity or a NaN, the nodes that do not see it are unaffected.
+ * mla_append_kv and mla_run_append take the plan as any other.  Where a node's latent row
+ * holds an infinity or a NaN, the nodes that do not see it are unaffected, and those that do
+ * get what the formula gives: a NaN throughout (lse too) where the score is +inf or a NaN,
+ * and where it is -inf a NaN in the columns whose ckv element is not finite.
  * Errors: as mla_plan, and INVALID_ARGUMENT for bad parents, a row with k_b < q_b, a
  * larger tree, or context_only. */
 mla_status mla_plan_tree(const mla_dims* dims, int32_t batch, const int32_t* qo_indptr, const int32_t* kv_indptr,

@@ -144,8 +144,9 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t a, uint32_t b, float f)
   return pack_bf16x2(x, y);
 }
 
-// Set the elements of a stage's ckv rows that are not finite to 0 (one warp).  A query that
-// sees such a key keeps the NaN of its own weight; the others must not meet 0 * NaN.
+// Set the elements of a stage's ckv rows that are not finite to 0 (one warp): queries that do
+// not see such a key must not meet 0 * NaN.  One that does see it has a NaN weight and sum,
+// or the weight 0 where its score is -inf: mark_non_finite then writes what 0 * inf is.
 __device__ __noinline__ void clear_non_finite(uint8_t* stage, int lane) {
   for (int i = lane; i < static_cast<int>(attn::kStageKpe / 16); i += 32) {
     uint4* piece = reinterpret_cast<uint4*>(stage + 16 * i);
@@ -163,6 +164,48 @@ __device__ __noinline__ void clear_non_finite(uint8_t* stage, int lane) {
   __syncwarp();
 }
 
+// A warp's staged output rows (tile rows 32 q + R) get the NaN that a visible key's non-finite
+// ckv element makes of its column, whatever the key's weight: 0 times an infinity is one too.
+// Called where a masked tile was cleared; looks at every key from the item's first masked tile
+// on.  Lane l owns columns [8 l, 8 l + 8) of the CTA's half.
+__device__ __noinline__ void mark_non_finite(const AttnParams& p, int rank, int q, uint8_t* stage, int lane) {
+  // (an append that this grid depends on is done once keys have landed, but not by this
+  // thread's own wait)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const WorkItem w = p.work[blockIdx.x >> 1];
+  const TreeItem ti = p.tree_items[blockIdx.x >> 1];
+  const int nrows = min(32, w.n_rows - 32 * q);
+  const bool wide = w.partial >= 0;  // fp32, else bf16
+  const int masked = ti.words > 0 ? ti.first_tile * kTileN : max(0, w.diag_base + 1) / kTileN * kTileN;
+  const int end = min(w.key_end, w.kv_len), P = p.page_size;
+  const size_t width = kCkv + p.rope_dim;
+  const __nv_bfloat16* cols = static_cast<const __nv_bfloat16*>(p.cache) + 256 * rank + 8 * lane;
+  for (int key = max(masked, w.key_begin); key < end; ++key) {
+    const size_t row = static_cast<size_t>(p.kv_indices[w.page_base + key / P]) * P + key % P;
+    const uint4 x = __ldcg(reinterpret_cast<const uint4*>(cols + row * width));
+    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+    uint32_t odd = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) odd |= ((v[i >> 1] >> (16 * (i & 1))) & 0x7f80u) == 0x7f80u ? 1u << i : 0u;
+    if (!__any_sync(0xffffffffu, odd != 0u)) continue;
+    for (int R = 0; R < nrows; ++R) {
+      const int i = (32 * q + R) / p.num_heads;  // token of the tile
+      const bool seen = ti.words > 0 ? (p.tree_words[ti.word_base + i * ti.words + key / kTileN - ti.first_tile] >>
+                                        (key % kTileN)) & 1
+                                     : key <= w.diag_base + i;
+      for (int e = 0; seen && e < 8; ++e) {
+        if (!((odd >> e) & 1)) continue;
+        if (wide)
+          *reinterpret_cast<uint32_t*>(stage + (R << 10) + (((2 * lane + (e >> 2)) ^ R) << 4) + 4 * (e & 3)) =
+              0x7fffffffu;
+        else
+          *reinterpret_cast<uint16_t*>(stage + (R << 9) + ((lane ^ R) << 4) + 2 * e) = 0x7fffu;
+      }
+    }
+  }
+  __syncwarp();
+}
+
 // Pipeline per 64-key tile j (phases of every two-buffer barrier are j >> 1):
 //   producer : KV(j) -> stage j % 3                        (after PV(j - 3) freed it)
 //   QK warp  : QK(j) -> S[j % 2], as soon as KV(j) landed and S(j - 2) was read
@@ -176,7 +219,7 @@ __device__ __noinline__ void clear_non_finite(uint8_t* stage, int lane) {
 template <bool kTree, bool kPace>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
     mla_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                    const __grid_constant__ CUtensorMap tm_kpe, const AttnParams p) {
+                    const __grid_constant__ CUtensorMap tm_kpe, const __grid_constant__ AttnParams p) {
   using namespace attn;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
@@ -199,10 +242,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
   // [j % 4]: j if tile j has a score that is not finite (tree steps).  A slot is written again
   // four tiles on, after the wait for PV(j + 1).
   volatile int* odd_tile = reinterpret_cast<volatile int*>(smem + kMisc + 16);
+  volatile int* odd_any = odd_tile + 4;  // 1 if some tile had one
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; kTree && i < 4; ++i) odd_tile[i] = -1;
+    if (kTree) *odd_any = 0;
     mbar_init(bar(bQFull), 1);
     mbar_init(bar(bQTmem), 4);
     for (int s = 0; s < kStages; ++s) {
@@ -328,6 +373,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
             const int c = i / n16, k = i % n16;
             *reinterpret_cast<float4*>(smem + kKV + st * kStageBytes + c * 8192 + first_bad * 128 + k * 16) = z;
           }
+          // (a tree step's kpe rows too: a score there must not look like a key's that is not
+          // finite)
+          for (int i = lane; kTree && p.rope_dim > 0 && i < 4 * (kTileN - first_bad); i += 32)
+            *reinterpret_cast<float4*>(smem + kKV + st * kStageBytes + kStageKpe + first_bad * 64 + i * 16) = z;
           fence_proxy_async_smem();
           __syncwarp();
         }
@@ -537,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
           float odd = 0.f;
 #pragma unroll
           for (int c = 0; c < 64; ++c) odd = fmaf(t[c], 0.f, odd);
-          if (odd != odd) odd_tile[j & 3] = j;
+          if (odd != odd) odd_tile[j & 3] = j, *odd_any = 1;
 #pragma unroll
           for (int c = 0; c < 64; ++c) t[c] = ((seen >> c) & 1) ? t[c] : kNegInf;
         }
@@ -676,6 +725,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(attn::kThreads, 1)
         }
         __syncwarp();
         const int nrows = min(32, w.n_rows - 32 * q);  // rows of this warp inside the tile
+        if (kTree && *odd_any != 0) mark_non_finite(p, rank, q, stage, lane);
         uint8_t* base = part ? static_cast<uint8_t*>(p.ws_o) + static_cast<size_t>(w.partial) * kCkv * 2
                              : static_cast<uint8_t*>(p.out) + static_cast<size_t>(w.q_row0) * kCkv * 2;
         for (int R = 0; wide && R < nrows; ++R) {
@@ -881,6 +931,7 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
   AttnParams p = a.p;
   p.q_nope = a.q_nope;
   p.q_pe = a.q_pe;
+  p.cache = a.cache;
   p.nan_guard = __builtin_nanf("");
   p.box_rows = p.page_size < kTileN ? p.page_size : kTileN;
   const uint32_t br = static_cast<uint32_t>(p.box_rows);

@@ -16,6 +16,7 @@ struct AttnParams {
   const int32_t* kv_indices;
   const void* q_nope;  // bf16 [T*H, 512] (the kernel reads part of Q directly)
   const void* q_pe;    // bf16 [T*H, 64]; unused when rope_dim == 0
+  const void* cache;   // bf16 [cache rows, 512 + rope_dim]
   void* out;         // bf16 [T*H, 512]
   float* lse;        // fp32 [T*H] or nullptr
   void* ws_o;        // bf16 [partials, 128, 512]
