@@ -417,7 +417,9 @@ def mla_run(plan: MlaPlan, q_nope, q_pe, cache, out=None, lse=None, return_lse: 
     """Run the planned attention (``mla_run``).  Returns ``out`` or ``(out, lse)``.
     With ``kv_new`` ([T, 512 + rope_dim] bf16) the step's latent rows are first written
     into the cache (``mla_run_append``).  ``q_pe`` may be None for a plan with
-    ``rope_dim=0``."""
+    ``rope_dim=0``.  ``stream`` is a stream's handle (None: torch's current one); outputs that
+    the call makes belong to that stream's memory, as if made under it, and work on other
+    streams is ordered behind the call by the caller."""
     N = _native()
     T, H, R = plan.token_capacity, plan.num_heads, plan.rope_dim
     # a tree plan's tensors must be on the current device (which is the plan's)
@@ -428,10 +430,10 @@ def mla_run(plan: MlaPlan, q_nope, q_pe, cache, out=None, lse=None, return_lse: 
     qpe_p = N.tensor(q_pe, "q_pe", _BF16, dev, (T, H, R)) if R > 0 or q_pe is not None else 0
     on = q_nope.get_device()
     if out is None:
-        out = N.empty(_BF16, on, rows)
+        out = N.empty(_BF16, on, rows, stream)
     out_p = N.tensor(out, "out", _BF16, dev, rows)
     if return_lse and lse is None:
-        lse = N.empty(_F32, on, (T, H))
+        lse = N.empty(_F32, on, (T, H), stream)
     lse_p = N.tensor(lse, "lse", _F32, dev, (T, H)) if lse is not None else 0
     if stream is None:
         stream = N.stream(on)
@@ -621,7 +623,8 @@ def mla_verify_tree(plan: MlaPlan, draft_tokens, target_probs, uniform, uniform_
     random numbers (``mla_verify_tree``).  ``target_probs`` and ``draft_probs`` (None:
     point masses) are [T, vocab] fp32 or bf16 with contiguous rows; ``draft_tokens`` [T]
     int32; ``uniform`` [T] and ``uniform_next`` [batch] fp32.  Returns (accept_index [T],
-    num_accepted [batch], next_token [batch]), int32."""
+    num_accepted [batch], next_token [batch]), int32.  ``stream`` and the outputs that the
+    call makes are as for ``mla_run``."""
     st, *out = _native().verify_tree(plan.handle.value, plan.token_capacity, plan.batch_capacity, draft_tokens,
                                      target_probs, uniform, uniform_next, draft_probs, accept_index, num_accepted,
                                      next_token, stream)

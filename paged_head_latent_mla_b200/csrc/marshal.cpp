@@ -9,6 +9,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
@@ -196,26 +197,50 @@ PyObject* cache_addresses(PyObject* o, const CacheShape& want) {
   return out;
 }
 
-// empty(type, dev, shape) -> a new tensor
+void* current_stream(int64_t dev) {
+  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+}
+
+// A new tensor whose memory belongs to the stream that the call runs on: torch's allocator
+// hands out what was freed on the same stream, so neither an earlier owner's work nor a later
+// one's can be under way on another.
+at::Tensor empty_on(at::IntArrayRef shape, int64_t type, int64_t dev, void* stream) {
+  const auto options = at::TensorOptions().dtype(kTypes[type]).device(at::kCUDA, dev);
+  if (stream == current_stream(dev)) return at::empty(shape, options);
+  const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(
+      static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(dev)));
+  return at::empty(shape, options);
+}
+
+// A stream argument: its handle, or None for the device's current stream.
+bool stream_of(PyObject* o, int64_t dev, void** s) {
+  if (o == Py_None) {
+    *s = current_stream(dev);
+    return true;
+  }
+  int64_t v;
+  if (!integer(o, &v)) return false;
+  *s = reinterpret_cast<void*>(v);
+  return true;
+}
+
+// empty(type, dev, shape, stream) -> a new tensor for a call on the stream
 PyObject* py_empty(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    if (!arity(n, 3)) return nullptr;
+    if (!arity(n, 4)) return nullptr;
     int64_t type, dev, shape[4];
     const Py_ssize_t dims = PyTuple_Size(a[2]);
     if (!integer(a[0], &type) || !integer(a[1], &dev) || dims < 0) return nullptr;
     if (dims > 4) return value_error("at most four dimensions");
     for (Py_ssize_t i = 0; i < dims; ++i)
       if (!integer(PyTuple_GET_ITEM(a[2], i), &shape[i])) return nullptr;
-    return THPVariable_Wrap(at::empty(at::IntArrayRef(shape, dims),
-                                      at::TensorOptions().dtype(kTypes[type]).device(at::kCUDA, dev)));
+    void* stream;
+    if (!stream_of(a[3], dev, &stream)) return nullptr;
+    return THPVariable_Wrap(empty_on(at::IntArrayRef(shape, dims), type, dev, stream));
   });
 }
 
 int64_t current_device() { return c10::cuda::device_count() > 0 ? c10::cuda::current_device() : -1; }
-
-void* current_stream(int64_t dev) {
-  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-}
 
 // device() -> the current CUDA device, -1 on a machine without one
 PyObject* py_device(PyObject*, PyObject*) {
@@ -260,18 +285,6 @@ bool bound() {
   if (g_verify && g_compact && g_copy) return true;
   PyErr_SetString(PyExc_RuntimeError, "the library's functions are not bound");
   return false;
-}
-
-// A stream argument: its handle, or None for the device's current stream.
-bool stream_of(PyObject* o, int64_t dev, void** s) {
-  if (o == Py_None) {
-    *s = current_stream(dev);
-    return true;
-  }
-  int64_t v;
-  if (!integer(o, &v)) return false;
-  *s = reinterpret_cast<void*>(v);
-  return true;
 }
 
 mla_plan_t plan_of(int64_t handle) { return reinterpret_cast<mla_plan_t>(handle); }
@@ -328,6 +341,8 @@ PyObject* py_verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!next) return nullptr;
     static const char* const kNames[] = {"accept_index", "num_accepted", "next_token"};
     const int64_t size[] = {T, B, B}, from[] = {0, T, T + B};
+    void* stream;
+    if (!stream_of(a[11], dev, &stream)) return nullptr;
     at::Tensor made, out[3];
     for (int i = 0; i < 3; ++i) {
       if (a[8 + i] != Py_None) {
@@ -336,14 +351,12 @@ PyObject* py_verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
         out[i] = *t;
         continue;
       }
-      if (!made.defined()) made = at::empty({T + 2 * B}, at::TensorOptions().dtype(at::kInt).device(at::kCUDA, dev));
+      if (!made.defined()) made = empty_on({T + 2 * B}, 2, dev, stream);
       auto impl = made.unsafeGetTensorImpl()->shallow_copy_and_detach(c10::VariableVersion(0), true);
       impl->set_storage_offset(from[i]);
       impl->set_sizes_contiguous({size[i]});
       out[i] = at::Tensor(std::move(impl));
     }
-    void* stream;
-    if (!stream_of(a[11], dev, &stream)) return nullptr;
     mla_status st;
     Py_BEGIN_ALLOW_THREADS;
     st = g_verify(plan_of(plan), static_cast<const int32_t*>(tokens->data_ptr()), target->data_ptr(), ld_target,

@@ -1,6 +1,8 @@
 """What a stream may rely on: the order of the library's launches among the stream's other
 work, and how long a plan's buffers stay its own where several streams use it."""
 
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -85,7 +87,8 @@ CALLS = ["append", "run_append", "verify", "compact"]
 
 class Step:
     """A tree plan over eight rows, and calls on it that two streams may make side by side
-    (each has outputs of its own; a compaction of the path (0,) moves nothing)."""
+    (each has outputs of its own, made beforehand: an allocation may wait for the device; a
+    compaction of empty paths moves nothing)."""
 
     def __init__(self, **kw):
         self.d = d = make_custom([4] * 8, [100] * 8, 16, 16, seed=52)
@@ -98,18 +101,20 @@ class Step:
         self.u = torch.zeros(32, device=DEV)
         self.acc = torch.full((32,), -1, dtype=torch.int32, device=DEV)
         self.cnt = torch.zeros(8, dtype=torch.int32, device=DEV)
+        self.out = torch.zeros_like(self.q[0])
+        self.verified = [[torch.zeros(n, dtype=torch.int32, device=DEV) for n in (32, 8, 8)] for _ in range(2)]
+        gc.collect()  # (a plan that is collected waits for its own calls)
         torch.cuda.synchronize()
 
-    def call(self, what, plan=None):
-        plan = plan or self.plan
+    def call(self, what, i=0):
         if what == "append":
-            M.mla_append_kv(plan, self.kv, self.cache)
+            M.mla_append_kv(self.plan, self.kv, self.cache)
         elif what == "run_append":
-            M.mla_run(plan, *self.q, self.cache, kv_new=self.kv)
+            M.mla_run(self.plan, *self.q, self.cache, out=self.out, kv_new=self.kv)
         elif what == "verify":
-            M.mla_verify_tree(plan, self.tok, self.probs, self.u, self.u[:8])
+            M.mla_verify_tree(self.plan, self.tok, self.probs, self.u, self.u[:8], None, *self.verified[i])
         else:
-            M.mla_compact_kv(plan, self.acc, self.cnt, [self.cache])
+            M.mla_compact_kv(self.plan, self.acc, self.cnt, [self.cache])
 
 
 @pytest.fixture(scope="module")
@@ -123,9 +128,9 @@ def loaded(lib):
 
 
 def delayed(stream, f):
-    """Enqueue f on the stream behind 50 ms or so of other work; the event after it."""
+    """Enqueue f on the stream behind 0.1 s or so of other work; the event after it."""
     with torch.cuda.stream(stream):
-        torch.cuda._sleep(100_000_000)
+        torch.cuda._sleep(200_000_000)
         f()
         return stream.record_event()
 
@@ -139,7 +144,7 @@ def test_a_plan_waits_for_its_calls_on_every_stream(first, after, loaded):
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
     done = delayed(a, lambda: step.call(first))
     with torch.cuda.stream(b):
-        step.call("verify")
+        step.call("verify", 1)
     assert not done.query()
     if after == "destroy":
         step.plan.destroy()
@@ -193,3 +198,45 @@ def test_a_captured_append_is_waited_for(loaded):
     assert done.query()
     torch.cuda.synchronize()
     del g
+
+
+# ------------------------------------------------------------------ outputs that a call makes
+@pytest.mark.parametrize("what", ["run", "verify"])
+def test_outputs_belong_to_the_stream_of_the_call(what, loaded):
+    """A call on a stream that is not torch's current one writes there: what the current
+    stream freed may still be in use on it, and what the call made is not the current
+    stream's to hand out once it is freed."""
+    step = Step()
+    s = torch.cuda.Stream()
+
+    def make(stream):
+        if what == "run":
+            return M.mla_run(step.plan, *step.q, step.cache, return_lse=True, stream=stream)
+        return M.mla_verify_tree(step.plan, step.tok, step.probs, step.u, step.u[:8], stream=stream)
+
+    want = [x.clone() for x in make(None)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    first = make(None)
+    freed = {x.untyped_storage().data_ptr() for x in first}
+    torch.cuda.synchronize()
+    del first  # (nothing is pending here: only the addresses are looked at)
+    got = make(s.cuda_stream)
+    s.synchronize()
+    there = {x.untyped_storage().data_ptr() for x in got}
+    assert not there & freed
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del got
+    again = make(None)
+    torch.cuda.synchronize()
+    assert not {x.untyped_storage().data_ptr() for x in again} & there
+    got = make(s.cuda_stream)  # (the stream itself uses its memory again)
+    assert {x.untyped_storage().data_ptr() for x in got} == there
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.cuda.stream(s):
+        assert all(torch.equal(a, b) for a, b in zip(make(s.cuda_stream), want))
+        assert all(torch.equal(a, b) for a, b in zip(make(None), want))
+    with torch.inference_mode():
+        assert all(torch.equal(a, b) for a, b in zip(make(None), want))
+    torch.cuda.synchronize()
