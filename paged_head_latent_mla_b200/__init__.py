@@ -184,17 +184,20 @@ _BF16, _F32, _I32 = 0, 1, 2
 
 
 def _native():
-    """The binding's native argument checks (built with the library)."""
+    """The binding's native argument checks, as built for this Python and torch."""
     global _helpers
     if _helpers is None:
-        import importlib
+        import importlib.util
 
-        import torch  # noqa: F401  (its libraries must be loaded first)
+        from . import _build
 
+        path = _build.marshal_path()  # (imports torch, whose libraries must be loaded first)
         try:
-            m = importlib.import_module("._marshal", __name__)
+            spec = importlib.util.spec_from_file_location(__name__ + "._marshal", path)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
         except ImportError as e:
-            raise RuntimeError("the binding's native part is missing or stale: python -m "
+            raise RuntimeError(f"the binding's native part {path} is missing or stale: python -m "
                                "paged_head_latent_mla_b200._build --force") from e
         lib = load_library()
         m.bind(*[ctypes.cast(f, ctypes.c_void_p).value

@@ -8,14 +8,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmla_b200.so")
 SOURCES = ["api.cu", "mla_attn.cu", "state_ops.cu", "spec_ops.cu", "plan.cpp", "noalloc.cu"]
-MARSHAL = os.path.join(PKG, "_marshal.so")  # the Python binding's argument checks
-MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")  # the Python binding's argument checks
 HEADERS = ["mla_internal.h", "mla_launch.h", "sm100_ptx.cuh"]
 
 
@@ -37,14 +37,22 @@ def needs_build() -> bool:
     return _older(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "mla.h")])
 
 
-def build_marshal(force: bool = False) -> str:
-    """Compile the binding's native part against the installed torch (host code only)."""
-    if not force and not _older(MARSHAL, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "mla.h")]):
-        return MARSHAL
-    import sysconfig
-
+def marshal_path() -> str:
+    """The binding's native part for this Python and torch.  It reads both's objects by their
+    layout, so another version's file must neither count as built nor be loaded: the name
+    says which ones it is for."""
     import torch
 
+    return os.path.join(PKG, "_marshal.torch-%s.%s.so" % (torch.__version__, sysconfig.get_config_var("SOABI")))
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile the binding's native part against the installed torch (host code only)."""
+    import torch
+
+    target = marshal_path()
+    if not force and not _older(target, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "mla.h")]):
+        return target
     home = os.path.dirname(torch.__file__)
     inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")]
@@ -52,13 +60,13 @@ def build_marshal(force: bool = False) -> str:
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi())]
     for d in inc:
         cmd += ["-isystem", d]
-    cmd += [MARSHAL_SOURCE, "-o", MARSHAL + ".tmp"]
+    cmd += [MARSHAL_SOURCE, "-o", target + ".tmp"]
     cmd += ["-L" + os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
-    os.replace(MARSHAL + ".tmp", MARSHAL)
-    return MARSHAL
+    os.replace(target + ".tmp", target)
+    return target
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
