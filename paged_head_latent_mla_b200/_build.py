@@ -1,9 +1,11 @@
 """Build the sm_100a shared library in-tree: paged_head_latent_mla_b200/libmla_b200.so.
 
 Run as ``python -m paged_head_latent_mla_b200._build``.  nvcc cross-compiles for
-sm_100a without a GPU present.
+sm_100a without a GPU present.  The library needs nvcc alone; the Python binding's native
+part is built after it where torch is installed (``--library-only``: not at all).
 """
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -69,10 +71,20 @@ def build_marshal(force: bool = False) -> str:
     return target
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_marshal(force)
-    if not force and not needs_build():
-        return LIB
+def build(force: bool = False, verbose: bool = False, library_only: bool = False) -> str:
+    """Build what is missing or older than its sources: the library, then the binding's native
+    part unless ``library_only`` (or without torch, which the binding cannot do without)."""
+    if force or needs_build():
+        _build_library(verbose)
+    if not library_only:
+        if importlib.util.find_spec("torch") is None:
+            sys.stderr.write("torch is not installed: only the library was built, not the Python binding's part\n")
+        else:
+            build_marshal(force)
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
     cmd = [
         nvcc_path(),
         "-gencode", "arch=compute_100a,code=sm_100a",
@@ -89,8 +101,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         sys.stderr.write(res.stderr)
     os.replace(LIB + ".tmp", LIB)
-    return LIB
 
 
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv, library_only="--library-only" in sys.argv))

@@ -1,6 +1,7 @@
 """The build of the library and of the Python binding's native part: what is built for what,
 and what needs what (host only)."""
 
+import sys
 import sysconfig
 
 import pytest
@@ -50,3 +51,43 @@ def test_the_native_part_of_another_torch_does_not_count_as_built(monkeypatch):
 
 class _Done:
     returncode, stdout, stderr = 0, "", ""
+
+
+def _recorded(monkeypatch):
+    """Compilers that only record that they were called."""
+    ran = []
+    monkeypatch.setattr(_build.subprocess, "run", lambda cmd, **kw: ran.append(cmd[0].split("/")[-1]) or _Done())
+    monkeypatch.setattr(_build.os, "replace", lambda a, b: None)
+    return ran
+
+
+def test_the_library_is_built_without_torch(monkeypatch, capsys):
+    ran = _recorded(monkeypatch)
+    monkeypatch.setattr(_build.importlib.util, "find_spec", lambda name: None)
+    monkeypatch.setitem(sys.modules, "torch", None)  # importing it fails
+    assert _build.build(force=True) == _build.LIB
+    assert ran == ["nvcc"] and "torch is not installed" in capsys.readouterr().err
+
+
+def test_the_library_alone_on_request(monkeypatch):
+    ran = _recorded(monkeypatch)
+    monkeypatch.setitem(sys.modules, "torch", None)
+    _build.build(force=True, library_only=True)
+    assert ran == ["nvcc"]
+
+
+def test_a_binding_that_does_not_compile_leaves_the_library(monkeypatch):
+    """(no Python.h, for instance)"""
+    ran = _recorded(monkeypatch)
+    done = _build.subprocess.run
+
+    def run(cmd, **kw):
+        out = done(cmd, **kw)
+        if cmd[0] == "g++":
+            out.returncode, out.stderr = 1, "Python.h: No such file"
+        return out
+
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    with pytest.raises(RuntimeError, match="Python.h"):
+        _build.build(force=True)
+    assert ran == ["nvcc", "g++"]
