@@ -376,10 +376,9 @@ mla_status mla_plan_describe_tree(mla_plan_t plan, int32_t* items, int32_t* node
 typedef enum { MLA_PROB_FP32 = 0, MLA_PROB_BF16 = 1 } mla_prob_type;
 
 /* Verify a step's drafted trees against the target's probabilities, from given random
- * numbers: the tokens that result are distributed as the target's own (recursive
- * rejection along the tree).  Row b's walk starts at its node 0, the row's last decided
- * token (other roots are never reached).  With p and q the target's and the draft's
- * weights at node v, w = p and Z = 1, the children c of v are tried in order:
+ * numbers, by recursive rejection along the tree.  Row b's walk starts at its node 0, the
+ * row's last decided token (other roots are never reached).  With p and q the target's and
+ * the draft's weights at node v, w = p and Z = 1, the children c of v are tried in order:
  *     x = draft_tokens[c];  accepted if  uniform[c] * q(x) * Z < w(x)
  *     else, before the next child:  w = max(w - Z q, 0),  Z = sum of w
  * and an accepted child is the next v.  Where every child was rejected (or v has none),
@@ -389,8 +388,17 @@ typedef enum { MLA_PROB_FP32 = 0, MLA_PROB_BF16 = 1 } mla_prob_type;
  * Without draft_probs the drafted tokens are point masses: a child is accepted if
  * uniform[c] * Z < w(x), else w(x) = 0 and Z = max(Z - w(x), 0).
  * A draft token < 0 was given, not drafted: it is accepted without a test.  One >= vocab
- * has weight 0.  Weights that are negative, infinite or NaN count as 0.  All sums and
- * comparisons are in 64 bits, in an order that does not change from call to call.
+ * has weight 0.  Weights that are negative, infinite or NaN count as 0.
+ * The tokens are distributed as the target's own where the uniforms are independent, siblings
+ * were drawn from the draft's row independently of one another (with replacement; without
+ * draft_probs they may be any tokens), and rows of weights sum to 1: every node starts from
+ * Z = 1.  Rows that miss 1 by the rounding of their type shift probabilities by about as much.
+ * All sums and comparisons are in 64 bits.  The order of a sum depends on the plan's rows (a
+ * graph plan's: its bucket's) and SMs and on the 16-byte alignment of the weights' rows, and
+ * on nothing else: the same call gives the same result, but a row verified in another batch
+ * or from another address may be decided otherwise at a border that is closer than the last
+ * bits of a sum.  The work per row is spread over as many blocks as the plan's rows leave
+ * room for, so a bucket that is mostly empty takes longer than a plan of the step's size.
  *   vocab         in [1, 2^28]
  *   draft_tokens  device int32 [T]; node 0's is not read
  *   target_probs  device [T] rows of `vocab` weights, row pitch ld_target (elements, >=
@@ -422,7 +430,9 @@ mla_status mla_verify_tree(mla_plan_t plan, const int32_t* draft_tokens, const v
  * num_accepted[b]) goes from key c_b + a to key c_b + k.  The row then holds c_b +
  * num_accepted[b] keys; its slots behind those are free.
  *   accept_index, num_accepted  device int32, as mla_verify_tree writes them (for each row
- *                 the entries increase); an entry outside [k, q_b) moves nothing
+ *                 the entries increase); an entry outside [k, q_b) moves nothing, nor does,
+ *                 in a graph replay (which is not checked), one whose slot or node's slot a
+ *                 later token of the step names too
  *   caches        host array of num_caches device pointers, each bf16
  *                 [num_pages][page_size][512 + rope_dim], none overlapping another
  * One launch per 128 caches, no allocation, no synchronisation.

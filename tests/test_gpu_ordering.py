@@ -240,3 +240,53 @@ def test_outputs_belong_to_the_stream_of_the_call(what, loaded):
     with torch.inference_mode():
         assert all(torch.equal(a, b) for a, b in zip(make(None), want))
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ replays are not checked
+def test_a_replayed_compaction_of_shared_slots_moves_what_the_plan_still_places():
+    """A step in which two rows' tokens name the same slots is refused by a call; a graph
+    captured on another step of the bucket moves only the rows of the later tokens."""
+    P = 16
+    apart = make_custom([3, 3], [20, 20], 16, P, seed=55, extra_pool_pages=2)
+    qo, kvp, kvi, last = tables(apart)
+    shared = kvi.clone()
+    shared[2:] = shared[:2]
+    kw = dict(num_heads=16, page_size=P, num_pages=apart.num_pages, sm_scale=apart.sm_scale)
+    parents = [-1, 0, 0] * 2
+    plan = M.mla_plan_tree(qo, kvp, kvi, last, parents, graph_max_batch=2, graph_max_tokens=6, graph_max_page_ids=8,
+                           **kw)
+    cache = apart.cache.to(DEV)
+    acc = torch.tensor([0, 2, -1, 0, 2, -1], dtype=torch.int32, device=DEV)
+    cnt = torch.full((2,), 2, dtype=torch.int32, device=DEV)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        M.mla_compact_kv(plan, acc, cnt, cache)
+    with torch.cuda.stream(s):
+        M.mla_plan_tree_update(plan, qo, kvp, shared, last, parents)
+        with pytest.raises(M.MlaError):
+            M.mla_compact_kv(plan, acc, cnt, cache)
+        g.replay()
+    s.synchronize()
+    want = apart.cache.clone()
+    page = int(shared[1])  # keys 17, 18 and 19 are its slots 1, 2 and 3
+    want[page, 2] = want[page, 3]
+    assert torch.equal(cache.cpu(), want)
+    del g
+    plan.destroy()
+
+
+def test_the_same_verification_gives_the_same_result():
+    """Weights whose sums round, in calls that share a plan's rows and buffers."""
+    rng = np.random.default_rng(56)
+    T, V = 40 * 9, 5003
+    d = make_custom([9] * 40, [9] * 40, 16, 16, seed=56, tables_only=True)
+    plan = M.mla_plan_tree(*tables(d), [-1, 0, 0, 0, 1, 1, 4, 4, 4] * 40, num_heads=16, page_size=16,
+                           num_pages=d.num_pages, sm_scale=d.sm_scale)
+    p, q = (torch.softmax(torch.from_numpy(rng.standard_normal((T, V)) * 2).float(), 1).to(DEV) for _ in range(2))
+    tok = torch.multinomial(q, 1).flatten().to(torch.int32)
+    u, un = torch.rand(T, device=DEV), torch.rand(40, device=DEV)
+    first = M.mla_verify_tree(plan, tok, p, u, un, draft_probs=q)
+    for _ in range(20):
+        again = M.mla_verify_tree(plan, tok, p, u, un, draft_probs=q)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
