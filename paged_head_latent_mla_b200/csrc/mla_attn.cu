@@ -782,19 +782,17 @@ __global__ void __launch_bounds__(256) mla_merge_kernel(const MergeParams p) {
   // 8 rows (one per warp) per block, or 4
   const int r = kTree ? ((blockIdx.x & 31) << 2) + (warp >> 1) : ((blockIdx.x & 15) << 3) + warp;
   const int half = kTree ? warp & 1 : 0;
-  if (r >= m.n_rows) {
-    // This grid may start before the attention grid is done, and what the stream holds next
-    // waits for this grid alone: it must not end first, as it would where every item is
-    // empty (a graph plan's step that splits nothing).  One block is enough to hold it.
-    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
+  // This grid may start before the attention grid is done, and what the stream holds next
+  // waits for this grid alone: it must not end first, as it would where every item is empty
+  // (a graph plan's step that splits nothing).  One block without rows is enough to hold it.
+  if (r >= m.n_rows && blockIdx.x != 0) return;
   const int n = m.n_refs;
   const int32_t* refs = p.refs + m.first_ref;  // workspace row of each partial's row 0
   int ref_l = lane < n ? refs[lane] : 0;       // lane u holds partial u's reference (u < 32)
   // Launched as a programmatic dependent of the attention grid: wait until that grid has
   // finished and its partials are visible.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (r >= m.n_rows) return;
   const float neg_inf = -__int_as_float(0x7f800000);
   float acc[kCols];
 #pragma unroll
