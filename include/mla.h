@@ -414,12 +414,13 @@ typedef enum { MLA_PROB_FP32 = 0, MLA_PROB_BF16 = 1 } mla_prob_type;
  *                 for a row without tokens
  *   next_token    device int32 [batch] (written): -1 for a row without tokens, or where no
  *                 weight is positive
+ * An output shares no memory with another output or an input.
  * For a graph plan T and batch are the bucket's bounds; entries behind the step's rows and
  * tokens are neither read nor written.  A row of more than MLA_TREE_MAX_NODES tokens is
  * refused with UNSUPPORTED (a graph replay, which is not checked, gives it num_accepted 0
  * and next_token -1).  One launch, no allocation, no synchronisation.
- * Errors: INVALID_ARGUMENT (NULL or misaligned pointer, vocab or pitch, not a tree plan),
- * UNSUPPORTED, CUDA. */
+ * Errors: INVALID_ARGUMENT (NULL, misaligned or overlapping pointers, vocab or pitch, not a
+ * tree plan), UNSUPPORTED, CUDA. */
 mla_status mla_verify_tree(mla_plan_t plan, const int32_t* draft_tokens, const void* target_probs, int64_t ld_target,
                            const void* draft_probs, int64_t ld_draft, int32_t vocab, mla_prob_type prob_type,
                            const float* uniform, const float* uniform_next, int32_t* accept_index,

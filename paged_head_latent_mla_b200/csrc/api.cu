@@ -852,6 +852,19 @@ mla_status mla_verify_tree(mla_plan_t p, const int32_t* draft_tokens, const void
   if (off(draft_tokens, 4) || off(uniform, 4) || off(uniform_next, 4) || off(accept_index, 4) || off(num_accepted, 4) ||
       off(next_token, 4))
     return MLA_ERR_INVALID_ARGUMENT;
+  {
+    // outputs are written while inputs are still read: none may share memory
+    const uintptr_t B = static_cast<uintptr_t>(p->sz.cap_rows), T = static_cast<uintptr_t>(p->sz.cap_tokens);
+    auto rows = [&](int64_t ld) { return T > 0 ? ((T - 1) * ld + vocab) * elem : 0; };
+    const std::pair<const void*, uintptr_t> part[] = {
+        {accept_index, 4 * T}, {num_accepted, 4 * B}, {next_token, 4 * B}, {draft_tokens, 4 * T}, {uniform, 4 * T},
+        {uniform_next, 4 * B}, {target_probs, rows(ld_target)}, {draft_probs, draft_probs ? rows(ld_draft) : 0}};
+    for (int o = 0; o < 3; ++o)
+      for (int i = o + 1; i < 8; ++i) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(part[o].first), y = reinterpret_cast<uintptr_t>(part[i].first);
+        if (x < y + part[i].second && y < x + part[o].second) return MLA_ERR_INVALID_ARGUMENT;
+      }
+  }
   if (p->layout.max_nodes > MLA_TREE_MAX_NODES) return MLA_ERR_UNSUPPORTED;
   VerifyParams v{};
   v.rows = p->d_tree<TreeRow>(p->sz.off_trows);

@@ -290,3 +290,26 @@ def test_the_same_verification_gives_the_same_result():
     for _ in range(20):
         again = M.mla_verify_tree(plan, tok, p, u, un, draft_probs=q)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+# ------------------------------------------------------------------ shared memory
+def test_verification_refuses_outputs_in_its_inputs():
+    """Outputs are written while inputs are read; rows of weights may be parts of one matrix."""
+    d = make_custom([3, 2], [3, 2], 16, 16, seed=57, tables_only=True)
+    plan = M.mla_plan_tree(*tables(d), [-1, 0, 0, -1, 0], num_heads=16, page_size=16, num_pages=d.num_pages,
+                           sm_scale=d.sm_scale)
+    both = torch.full((5, 64), 1 / 32, device=DEV)
+    ints = torch.zeros(32, dtype=torch.int32, device=DEV)
+    f = torch.zeros(16, device=DEV)
+    good = dict(draft_tokens=ints[:5], uniform=f[:5], uniform_next=f[5:7], target_probs=both[:, :32],
+                draft_probs=both[:, 32:], accept_index=ints[5:10], num_accepted=ints[10:12], next_token=ints[12:14])
+    out = M.mla_verify_tree(plan, **good)
+    assert out[0].data_ptr() == ints[5:].data_ptr() and ints[5:14].tolist() == [0, 1, -1, 0, 1, 2, 2, 0, 0]
+    as_ints = both.view(torch.int32).view(-1)
+    for bad in [dict(accept_index=ints[:5]), dict(accept_index=ints[4:9]), dict(num_accepted=ints[9:11]),
+                dict(next_token=ints[11:13]), dict(next_token=f.view(torch.int32)[6:8]),
+                dict(num_accepted=f.view(torch.int32)[4:6]), dict(accept_index=as_ints[64 * 4 + 31:][:5]),
+                dict(next_token=as_ints[64 * 5 - 2:])]:
+        with pytest.raises(M.MlaError) as e:
+            M.mla_verify_tree(plan, **{**good, **bad})
+        assert e.value.status == M.MLA_ERR_INVALID_ARGUMENT
