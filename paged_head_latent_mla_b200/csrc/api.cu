@@ -47,7 +47,7 @@ struct mla_plan_s {
   } sz;
   void* d_blob = nullptr;
   bool blob_fresh = false;  // the blob's status word has not been cleared yet
-  uint8_t* d_ws = nullptr;  // [ws rows][512] bf16 o, then [ws rows] fp32 lse
+  uint8_t* d_ws = nullptr;  // [ws rows][512] bf16 (tree plans: fp32) o, then [ws rows] fp32 lse
   // pinned staging, double-buffered so an update need not wait for the latest upload
   void* h_staging[2] = {nullptr, nullptr};
   size_t staging_cap[2] = {0, 0};

@@ -946,8 +946,9 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t stream) {
     tm_kpe = tm_kv;
   }
   // A tree step paces its idle quarters where its items have them throughout (64 rows of one
-  // node, 64 heads, 4096 keys: 112 us without, 98 with); full items do without that code (4
-  // rows of 257 nodes, 64 heads: 573 us, 578 with it).
+  // node, 64 heads, 4096 keys: 104 us without, 92 with); full items do without that code (4
+  // rows of 257 nodes, 64 heads, 1000 to 4096 keys: 405 us, 419 with it).  A graph keeps the
+  // kernel of the step it was captured on: right for every step of its bucket, at that cost.
   const auto kernel = p.tree_items == nullptr ? mla_attn_kernel<false, true>
                       : a.few_rows            ? mla_attn_kernel<true, true>
                                               : mla_attn_kernel<true, false>;

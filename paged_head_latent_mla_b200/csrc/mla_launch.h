@@ -19,8 +19,8 @@ struct AttnParams {
   const void* cache;   // bf16 [cache rows, 512 + rope_dim]
   void* out;         // bf16 [T*H, 512]
   float* lse;        // fp32 [T*H] or nullptr
-  void* ws_o;        // bf16 [partials, 128, 512]
-  float* ws_lse;     // fp32 [partials, 128]
+  void* ws_o;        // bf16 (of a tree plan fp32) [partial rows, 512]
+  float* ws_lse;     // fp32 [partial rows]
   int32_t* status;   // device status word
   int32_t* status_mirror;  // host-mapped pinned copy of the first error recorded, or null
   float scale_log2;  // sm_scale * log2(e)

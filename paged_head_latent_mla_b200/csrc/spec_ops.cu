@@ -34,14 +34,14 @@ namespace {
 // vocabulary would move a border by more than a token's weight.  Every sum has one fixed
 // order.
 //
-// Measured (device time, replayed from a graph): one chain over 32768 fp32 tokens 10 us,
-// 64 trees of 16 nodes over 131072 fp32 tokens 25.7 us (10.3 us of bytes at the copy rate),
-// 128 point-mass trees over 65537 bf16 tokens 12.4 us (2.6).  A call with one pass is a
+// Measured (device time, replayed from a graph): one chain of five over 32768 fp32 tokens
+// 10.2 us (three passes), 64 trees of 16 nodes over 131072 fp32 tokens 24.9 us (10.3 us of
+// bytes at the copy rate), 128 point-mass trees over 65537 bf16 tokens 12.5 us (2.6).  A call with one pass is a
 // chain of about ten dependent memory latencies (the gather's three, the pass, two cluster
 // barriers, the crossing).  Rows with several rejections then bound a batch: their passes
 // follow one another, about 4 us each over 131072 tokens, with two warps to a scheduler.
-// 512-thread blocks (28.3 us), two chunks in flight instead of four (29.6) and clusters
-// beyond what is resident (34.4) are slower.
+// Measured when the 64 trees took 26.7 us: 512-thread blocks 28.3, two chunks in flight
+// instead of four 29.6, clusters beyond what is resident 34.4.
 constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kVBlocksPerSm = 4;
@@ -685,12 +685,14 @@ static_assert(sizeof(VerifyShared) <= 48 * 1024, "fits without an opt-in");
 
 cudaError_t launch_verify(const VerifyParams& p, int rows, bool bf16, int num_sms, cudaStream_t stream) {
   // As many blocks to a row as keep every cluster resident at once: 64 rows over 131072
-  // tokens take 26.7 us with 8, 33.0 with 4 and 52 with 2 blocks; 512 rows over 32768 bf16
-  // tokens 36 us with 1 and 67 with 8.
+  // tokens take 24 us with 8, 29 with 4 and 44 with 2 blocks; 512 rows over 32768 bf16
+  // tokens 27 us with 1 and 57 with 8.  `rows` is a graph plan's bucket, whatever its step
+  // holds: 64 rows take 18 us in a bucket of 64, 28 in one of 256 and 59 in one of 512
+  // (another draw of the same sizes).
   int cluster = kVMaxCluster;
   while (cluster > 1 && static_cast<int64_t>(rows) * cluster > int64_t(kVBlocksPerSm) * num_sms) cluster /= 2;
   // Whole 16-byte loads where p's and q's rows have the same offset from a 16-byte boundary
-  // (64 rows over 131072 tokens 26.7 us, element by element 36.2).
+  // (64 rows over 131072 tokens 24 us, element by element 33).
   const int64_t es = bf16 ? 2 : 4;
   const bool vec = !p.draft || (((p.ld_target - p.ld_draft) * es) % 16 == 0 &&
                                 ((reinterpret_cast<uintptr_t>(p.target) ^ reinterpret_cast<uintptr_t>(p.draft)) & 15u) == 0);
