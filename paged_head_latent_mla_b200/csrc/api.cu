@@ -289,9 +289,8 @@ void quiesce(mla_plan_s* p) {
     // graphs captured from the plan may have replayed on any stream
     cudaDeviceSynchronize();
     cudaGetLastError();
-  } else {
-    wait_uses(p);
   }
+  wait_uses(p);  // (also where another device is current)
   for (int i = 0; i < 2; ++i)
     if (p->ev_upload[i] && p->upload_pending[i]) cudaEventSynchronize(p->ev_upload[i]);
 }
