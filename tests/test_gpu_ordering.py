@@ -128,9 +128,9 @@ def loaded(lib):
 
 
 def delayed(stream, f):
-    """Enqueue f on the stream behind 0.1 s or so of other work; the event after it."""
+    """Enqueue f on the stream behind 0.3 s or so of other work; the event after it."""
     with torch.cuda.stream(stream):
-        torch.cuda._sleep(200_000_000)
+        torch.cuda._sleep(600_000_000)
         f()
         return stream.record_event()
 
